@@ -85,7 +85,7 @@ static bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a -
 // Plan the page layout: latent blocks in order (keys per KV head, then values),
 // each a multiple of 16 bytes; a quantized block is the scale block
 // [group][slot] fp16 followed by one LSB-first code block per group.
-static starkv_status plan_layer(starkv_layer* L) {
+static starkv_status plan_layer(starkv_layer* L, int kv_bits) {
   const starkv_layer_config& c = L->cfg;
   const int Hkv = c.n_kv_heads, d = c.head_dim;
   const int es = c.dtype == STARKV_F32 ? 4 : 2;
@@ -97,7 +97,10 @@ static starkv_status plan_layer(starkv_layer* L) {
     for (int h = 0; h < Hkv; ++h) widths.push_back(L->key_ranks[h]);
     widths.push_back(c.value_rank);
   }
-  const bool quant = c.quantized && !c.plain;
+  // an uncompressed layer's codes: every channel at kv_bits, groups of 32 (starkv_load_plain)
+  const bool quant = (c.quantized && !c.plain) || kv_bits;
+  const float top_fraction = kv_bits ? 1.f : c.top_fraction;
+  const int top_bits = kv_bits ? kv_bits : c.top_bits, group_size = kv_bits ? 32 : c.group_size;
   size_t off = 0;
   int ch = 0;
   double bpt = 0;
@@ -117,15 +120,15 @@ static starkv_status plan_layer(starkv_layer* L) {
       off += ru((size_t)kPage * ld.width * es, 16);
       bpt += (double)ld.width * es;
     } else {
-      const int nh = n_high(ld.width, c.top_fraction);
-      const int seg_start[2] = {0, nh}, seg_len[2] = {nh, ld.width - nh}, seg_bits[2] = {c.top_bits, c.bottom_bits};
+      const int nh = n_high(ld.width, top_fraction);
+      const int seg_start[2] = {0, nh}, seg_len[2] = {nh, ld.width - nh}, seg_bits[2] = {top_bits, c.bottom_bits};
       std::vector<GroupDesc> gs;
       for (int s = 0; s < 2; ++s)
-        for (int k = 0; k < seg_len[s]; k += c.group_size)
-          gs.push_back(GroupDesc{seg_start[s] + k, std::min(c.group_size, seg_len[s] - k), seg_bits[s], 0});
+        for (int k = 0; k < seg_len[s]; k += group_size)
+          gs.push_back(GroupDesc{seg_start[s] + k, std::min(group_size, seg_len[s] - k), seg_bits[s], 0});
       ld.n_groups = (int)gs.size();
       ld.n_hi = nh;
-      ld.gsize = c.group_size;
+      ld.gsize = group_size;
       ld.scale_bytes = (int)ru((size_t)gs.size() * kPage * 2, 16);
       size_t boff = ld.scale_bytes;
       for (auto& g : gs) {
@@ -155,9 +158,10 @@ static starkv_status plan_layer(starkv_layer* L) {
   v.es = es;
   v.dtype = c.dtype;
   v.quantized = quant ? 1 : 0;
+  v.kv_bits = kv_bits;
   v.plain = c.plain ? 1 : 0;
   v.rope = c.rope ? 1 : 0;
-  v.hadamard = (quant && c.hadamard_block) ? 1 : 0;
+  v.hadamard = (quant && !c.plain && c.hadamard_block) ? 1 : 0;
   v.rope_log2_theta = (float)log2(c.rope_theta);
   const float sc = c.softmax_scale > 0 ? c.softmax_scale : (float)(1.0 / sqrt((double)d));
   v.scale_log2 = sc * kLog2e;
@@ -243,6 +247,8 @@ void starkv_free_layer(starkv_layer* L) {
   cudaFree(L->Bk_tiles);
   cudaFree(L->Wo_tiles);
   cudaFree(L->status);
+  cudaFree(L->norms);
+  cudaFree(L->turn);
   cudaFree(L->d_items);
   cudaFree(L->d_score_heads);
   cudaFree(L->rope_E);
@@ -251,9 +257,18 @@ void starkv_free_layer(starkv_layer* L) {
   delete L;
 }
 
-starkv_status starkv_load_factors(const starkv_layer_config* cfg, const void* A_k, const void* B_k, const void* A_v,
-                                  const void* B_v, const void* W_o, starkv_stream_t stream, starkv_layer** out) {
-  set_error("");
+}  // extern "C"
+
+// What starkv_load_plain adds to a layer.
+struct PlainOpts {
+  int kv_bits;
+  const void *q_norm, *k_norm;
+  float norm_eps;
+};
+
+static starkv_status load_layer(const starkv_layer_config* cfg, const PlainOpts* opts, const void* A_k, const void* B_k,
+                                const void* A_v, const void* B_v, const void* W_o, starkv_stream_t stream,
+                                starkv_layer** out) {
   CHECK_ARG(out != nullptr, "out is NULL");
   *out = nullptr;
   starkv_status st = check_config(cfg);
@@ -266,7 +281,7 @@ starkv_status starkv_load_factors(const starkv_layer_config* cfg, const void* A_
   if (!cfg->plain) L->key_ranks.assign(cfg->key_ranks, cfg->key_ranks + cfg->n_kv_heads);
   L->cfg.key_ranks = nullptr;
   cudaGetDevice(&L->device);
-  plan_layer(L);
+  plan_layer(L, opts ? opts->kv_bits : 0);
   LayerView& v = L->view;
   const int D = v.D, d = v.d, H = v.H;
   const size_t es = cfg->dtype == STARKV_F32 ? 4 : 2;
@@ -309,6 +324,25 @@ starkv_status starkv_load_factors(const starkv_layer_config* cfg, const void* A_
       (L->M_T && cfg->dtype != STARKV_F32 && cudaMemsetAsync(L->M_T, 0, 2 * (size_t)L->Dp * L->Kp, s)) ||
       (L->Wo_tiles && cudaMemsetAsync(L->Wo_tiles, 0, wo_tiles_bytes, s)))
     return fail(STARKV_ERR_CUDA, "upload tables");
+  if (opts) {
+    v.opt = 1;
+    v.norm_eps = opts->norm_eps;
+    if (opts->q_norm || opts->k_norm) {
+      if (cudaMalloc(&L->norms, sizeof(float) * 2 * (size_t)d) != cudaSuccess) return fail(STARKV_ERR_OOM, "cudaMalloc");
+      if (launch_norms_f32(opts->q_norm, opts->k_norm, cfg->dtype, d, L->norms, s) != cudaSuccess)
+        return fail(STARKV_ERR_CUDA, "norm weights");
+      v.q_norm = opts->q_norm ? L->norms : nullptr;
+      v.k_norm = opts->k_norm ? L->norms + d : nullptr;
+    }
+    if (cfg->rope) {
+      std::vector<double> turn(d / 2);
+      for (int p = 0; p < d / 2; ++p) turn[p] = pow(cfg->rope_theta, -2.0 * p / d) / (2.0 * M_PI);
+      if (cudaMalloc(&L->turn, sizeof(double) * turn.size()) != cudaSuccess) return fail(STARKV_ERR_OOM, "cudaMalloc");
+      if (cudaMemcpy(L->turn, turn.data(), sizeof(double) * turn.size(), cudaMemcpyHostToDevice) != cudaSuccess)
+        return fail(STARKV_ERR_CUDA, "rotation frequencies");
+      v.turn = L->turn;
+    }
+  }
   // Projection rows A_T[ch][k] for every latent channel (keys, then values).
   if (cfg->plain) {
     if (launch_transpose_into(A_k, D, v.Rk, cfg->dtype, L->A_T, 0, D, s) ||
@@ -385,6 +419,30 @@ starkv_status starkv_load_factors(const starkv_layer_config* cfg, const void* A_
   return STARKV_OK;
 }
 
+extern "C" {
+
+starkv_status starkv_load_factors(const starkv_layer_config* cfg, const void* A_k, const void* B_k, const void* A_v,
+                                  const void* B_v, const void* W_o, starkv_stream_t stream, starkv_layer** out) {
+  set_error("");
+  return load_layer(cfg, nullptr, A_k, B_k, A_v, B_v, W_o, stream, out);
+}
+
+starkv_status starkv_load_plain(const starkv_layer_config* cfg, int kv_bits, const void* q_norm, const void* k_norm,
+                                float norm_eps, const void* W_k, const void* W_v, const void* W_o,
+                                starkv_stream_t stream, starkv_layer** out) {
+  set_error("");
+  CHECK_ARG(out != nullptr, "out is NULL");
+  *out = nullptr;
+  CHECK_ARG(cfg != nullptr, "config is NULL");
+  CHECK_ARG(cfg->plain, "config must describe an uncompressed layer (plain = 1)");
+  CHECK_ARG(kv_bits == 0 || kv_bits == 8 || kv_bits == 4, "kv_bits must be 0, 8 or 4");
+  CHECK_ARG(kv_bits == 0 || cfg->head_dim == 64 || cfg->head_dim == 128 || cfg->head_dim == 256,
+            "a quantised cache needs head_dim 64, 128 or 256");
+  CHECK_ARG(norm_eps >= 0.f && norm_eps <= 1.f, "norm_eps must be in [0, 1]");
+  const PlainOpts opts{kv_bits, q_norm, k_norm, norm_eps};
+  return load_layer(cfg, &opts, W_k, nullptr, W_v, nullptr, W_o, stream, out);
+}
+
 starkv_status starkv_layer_get_info(const starkv_layer* L, starkv_layer_info* info) {
   CHECK_ARG(L && info, "NULL argument");
   info->n_latents = L->view.L;
@@ -452,6 +510,27 @@ starkv_status starkv_append(const starkv_layer* L, void* pool, int64_t n_pages, 
       CUDA_TRY(launch_project(L, input, n_tokens, (float*)workspace, s));
     }
     z = (const float*)workspace;
+  }
+  if (!input_is_latent && L->view.opt) {
+    // keys normed and rotated, keys and values stored or quantised in one pass over the projections
+    KvArgs a{};
+    a.v = L->view;
+    a.pool = (uint8_t*)pool;
+    a.n_pages = n_pages;
+    a.pt = page_table;
+    a.n_seqs = n_seqs;
+    a.max_pages = max_pages;
+    a.n = n_tokens;
+    a.seq_idx = seq_idx;
+    a.slots = a.positions = positions;
+    a.turn = L->view.turn;
+    a.k = z;
+    a.vv = z + L->view.Rk;
+    a.k_ld = a.v_ld = L->view.Ltot;
+    a.rotate = L->view.rope;
+    a.vec = L->view.d % 4 == 0;
+    CUDA_TRY(launch_qkv(a, true, s));
+    return STARKV_OK;
   }
   const int rotate = (!input_is_latent && L->view.hadamard) ? 1 : 0;
   const int rope_keys = (!input_is_latent && L->view.plain && L->view.rope) ? 1 : 0;

@@ -57,10 +57,38 @@ __global__ void k_qprep(LayerView v, const T* __restrict__ q, RowInfo ri, float*
   const int row = blockIdx.x, h = blockIdx.y, d = v.d, half = d / 2;
   const T* qh = q + ((size_t)row * v.H + h) * d;
   float* o = qrot + ((size_t)row * v.H + h) * d;
+  if (ri.row_hist && !ri.node_pos) {   // queries are normed and rotated already
+    for (int p = threadIdx.x; p < d; p += blockDim.x) o[p] = ldf(qh, p) * v.scale_log2;
+    return;
+  }
   const int pos = row_pos_of(ri, row);
+  float inv = 1.f;
+  if (v.q_norm) {
+    __shared__ float red[2];
+    float s = 0.f;
+    for (int p = threadIdx.x; p < d; p += blockDim.x) {
+      const float x = ldf(qh, p);
+      s += x * x;
+    }
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    inv = 1.f / sqrtf((red[0] + red[1]) / (float)d + v.norm_eps);
+  }
   for (int p = threadIdx.x; p < half; p += blockDim.x) {
     float a = ldf(qh, p), b = ldf(qh, p + half);
-    if (v.rope) {
+    if (v.q_norm) {
+      a *= inv * v.q_norm[p];
+      b *= inv * v.q_norm[p + half];
+    }
+    if (v.rope && v.opt) {
+      double sn, cs;
+      const double t = (double)pos * v.turn[p];
+      sincospi(2.0 * (t - rint(t)), &sn, &cs);
+      const float a2 = (float)(a * cs - b * sn), b2 = (float)(b * cs + a * sn);
+      a = a2;
+      b = b2;
+    } else if (v.rope) {
       double sn, cs;
       sincos((double)pos * rope_freq(p, d, v.rope_log2_theta), &sn, &cs);
       const float a2 = (float)(a * cs - b * sn), b2 = (float)(b * cs + a * sn);
@@ -112,8 +140,11 @@ __global__ void k_scores(LayerView v, const uint8_t* __restrict__ pool, long lon
       __syncthreads();
       for (int idx = threadIdx.x; idx < nt * half; idx += blockDim.x) {
         const int t = idx / half, p = idx % half;
+        // a drafted node's key stands at the node's position, not at its slot
+        const int hist = ri.row_hist ? ri.row_hist[row] : 0;
+        const int kpos = ri.node_pos && t0 + t >= hist ? ri.node_pos[ri.node_off[b] + (t0 + t - hist)] : t0 + t;
         double sn, cs;
-        sincos((double)(t0 + t) * rope_freq(p, d, v.rope_log2_theta), &sn, &cs);
+        sincos((double)kpos * rope_freq(p, d, v.rope_log2_theta), &sn, &cs);
         const float a = Kt[t * d + p], bb = Kt[t * d + p + half];
         Kt[t * d + p] = (float)(a * cs - bb * sn);
         Kt[t * d + p + half] = (float)(bb * cs + a * sn);
@@ -126,6 +157,10 @@ __global__ void k_scores(LayerView v, const uint8_t* __restrict__ pool, long lon
     const float* qh = qrot + ((size_t)row * v.H + h) * d;
     float acc = 0.f;
     for (int p = 0; p < d; ++p) acc += qh[p] * Kt[t * d + p];
+    if (ri.row_hist) {
+      const int j = t0 + t - ri.row_hist[row];
+      if (j >= 0 && !tree_sees(ri.mask, ri.mask_words, row, ri.row_node[row], j)) acc = -FLT_MAX;
+    }
     S[((size_t)row * v.H + h) * S_ld + t0 + t] = acc;
   }
 }
@@ -179,7 +214,10 @@ __global__ void k_value(LayerView v, const uint8_t* __restrict__ pool, long long
       for (int idx = threadIdx.x; idx < 32 * nhc; idx += blockDim.x) {
         const int t = idx % 32, k = idx / 32;
         float p = 0.f;
-        if (t < ntk) p = exp2f(S[((size_t)row * v.H + hbase + h0 + k) * S_ld + tt + t] - m_s[k]);
+        if (t < ntk) {
+          const float s = S[((size_t)row * v.H + hbase + h0 + k) * S_ld + tt + t];
+          p = s == -FLT_MAX ? 0.f : exp2f(s - m_s[k]);
+        }
         p_s[t][k] = p;
       }
       __syncthreads();
@@ -194,7 +232,8 @@ __global__ void k_value(LayerView v, const uint8_t* __restrict__ pool, long long
             z = latent_value(v, pool + (size_t)page * v.page_bytes + ld.block_off, ld, tok % kPage, c);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (k < nhc) acc[k] += p_s[t][k] * z;
+            // a masked node's value is not read into the sum, whatever it holds
+            if (k < nhc && !(ri.row_hist && p_s[t][k] == 0.f)) acc[k] += p_s[t][k] * z;
         }
       }
       __syncthreads();
@@ -262,7 +301,8 @@ __global__ void k_combine_tiled(LayerView v, int n_splits, const float* __restri
 // out[row][n] = sum_k y[row][k] * M_T[n][k]; one warp per output column, eight rows per pass.
 template <typename TY, typename TO>
 __global__ void k_out(const TY* __restrict__ y, const TY* __restrict__ MT, int rows, int K, int D,
-                      TO* __restrict__ out) {
+                      const int32_t* __restrict__ n_rows, TO* __restrict__ out) {
+  if (n_rows) rows = min(rows, *n_rows);
   const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (warp >= D) return;
   const TY* m = MT + (size_t)warp * K;
@@ -365,7 +405,8 @@ cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, lo
   const size_t smem = sizeof(float) * kTile * (size_t)(rmax + v.d);
   cudaError_t e = set_smem_limit((const void*)k_scores, smem);
   if (e != cudaSuccess) return e;
-  if (plain_decode_supported(v) && !tc_scores) {
+  const bool plain = plain_decode_supported(v) && !tc_scores && !ri.row_hist;
+  if (plain) {
     // uncompressed bf16 layer: one streaming pass over K and V, partials for the merge below
     e = launch_plain_decode(L, pool, n_pages, page_table, max_pages, rows, ri, qrot, p.n_splits, p.chunk, pY, pm, pl,
                             s);
@@ -380,7 +421,7 @@ cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, lo
     k_scores<<<dim3((max_len + kTile - 1) / kTile, v.Hkv, rows), 256, smem, s>>>(
         v, pool, n_pages, page_table, max_pages, ri, L->Bk, L->d_key_off, qrot, S, p.S_ld);
   }
-  if (!(plain_decode_supported(v) && !tc_scores)) {
+  if (!plain) {
     const int vb = value_block(v);
     const int cblocks = (v.rv + vb - 1) / vb;
     k_value<<<dim3(cblocks, p.n_splits, rows), kVBlock, 0, s>>>(v, pool, n_pages, page_table, max_pages, ri, S,
@@ -389,7 +430,7 @@ cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, lo
   if (v.dtype == STARKV_F32) {
     k_combine<float><<<dim3(rows, v.H), 128, 0, s>>>(v, ri, p.n_splits, pY, pm, pl, (float*)y);
     k_out<float, float><<<(v.D * 32 + 255) / 256, 256, 0, s>>>((const float*)y, (const float*)L->M_T, rows,
-                                                                v.H * v.wv, v.D, (float*)out);
+                                                                v.H * v.wv, v.D, ri.n_rows, (float*)out);
     return cudaGetLastError();
   }
   const int NB = outproj_nb(rows);
@@ -402,7 +443,78 @@ cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, lo
   k_combine_tiled<<<dim3(rows, v.H), 128, 0, s>>>(v, p.n_splits, pY, pm, pl, NB, KT, (uint8_t*)y);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_outproj_tc(L, y, rows, out, (float*)(w + p.part), s);
+  return launch_outproj_tc(L, y, rows, out, (float*)(w + p.part), s, ri.n_rows);
+}
+
+namespace {
+
+// A tree call's rows go through the row kernels in batches of at most this many, so that their score buffer (one fp32
+// per row, head and slot) stays bounded.
+constexpr int kTreeRows = 64;
+
+// Row tables of a tree call: row -> sequence, visible length, position, history, node.  One thread per row; rows that
+// belong to no sequence get length 0.  n_rows[c]: rows in use of batch c.
+__global__ void k_tree_rows(LayerView v, const int32_t* __restrict__ hist, const int32_t* __restrict__ node_off,
+                            int batch, int n_nodes, int max_nodes, int cap, const int32_t* __restrict__ q_pos,
+                            int32_t* __restrict__ row_seq, int32_t* __restrict__ row_len, int32_t* __restrict__ row_pos,
+                            int32_t* __restrict__ row_hist, int32_t* __restrict__ row_node,
+                            int32_t* __restrict__ n_rows) {
+  const int r = blockIdx.x * blockDim.x + threadIdx.x;
+  if (r >= n_nodes) return;
+  if (r % kTreeRows == 0)
+    n_rows[r / kTreeRows] = min(max(min(node_off[batch], n_nodes) - r, 0), kTreeRows);
+  int32_t seq = 0, len = 0, h = 0, node = 0;
+  for (int b = 0; b < batch; ++b) {
+    if (r < node_off[b] || r >= node_off[b + 1]) continue;
+    const TreeSeq q = tree_seq(hist, node_off, b, n_nodes, max_nodes, cap, v.status, r == node_off[b]);
+    seq = b;
+    len = q.cnt ? q.hist + q.cnt : 0;
+    h = q.hist;
+    node = r - q.off;
+    break;
+  }
+  row_seq[r] = seq;
+  row_len[r] = len;
+  row_pos[r] = q_pos ? q_pos[r] : 0;
+  row_hist[r] = h;
+  row_node[r] = node;
+}
+
+size_t tree_tab_bytes(int n_nodes) {
+  return ru256(sizeof(int32_t) * (5 * (size_t)n_nodes + (size_t)(n_nodes + kTreeRows - 1) / kTreeRows));
+}
+
+}  // namespace
+
+size_t tree_generic_ws_bytes(const starkv_layer* L, int max_ctx, int n_nodes) {
+  return tree_tab_bytes(n_nodes) + decode_generic_ws_bytes(L, std::min(n_nodes, kTreeRows), max_ctx, false);
+}
+
+// Every node as one row of the CUDA-core kernels, with its mask.
+cudaError_t launch_tree_generic(const starkv_layer* L, const TreeArgs& t, void* ws, size_t ws_bytes, cudaStream_t s) {
+  const int n = t.n_nodes, max_len = t.max_pages * kPage;
+  int32_t* tab = (int32_t*)ws;
+  const size_t tab_bytes = tree_tab_bytes(n);
+  if (ws_bytes < tree_generic_ws_bytes(L, max_len, n)) return cudaErrorInvalidValue;
+  k_tree_rows<<<(n + 127) / 128, 128, 0, s>>>(L->view, t.hist, t.node_off, t.batch, n, t.max_nodes, max_len, t.q_pos,
+                                              tab, tab + n, tab + 2 * n, tab + 3 * n, tab + 4 * n, tab + 5 * n);
+  cudaError_t e = cudaGetLastError();
+  const size_t es = L->view.dtype == STARKV_F32 ? 4 : 2;
+  for (int r0 = 0; r0 < n && e == cudaSuccess; r0 += kTreeRows) {
+    RowInfo ri{tab + r0, tab + n + r0, tab + 2 * n + r0};
+    ri.row_hist = tab + 3 * n + r0;
+    ri.row_node = tab + 4 * n + r0;
+    ri.n_rows = tab + 5 * n + r0 / kTreeRows;
+    ri.mask = t.mask ? t.mask + (size_t)r0 * t.mask_words : nullptr;
+    ri.mask_words = t.mask_words;
+    ri.node_off = t.node_off;
+    ri.node_pos = t.q_pos;
+    e = launch_decode_generic(L, t.pool, t.n_pages, t.pt, t.max_pages, std::min(kTreeRows, n - r0), ri, max_len,
+                              (const char*)t.q + (size_t)r0 * L->view.H * L->view.d * es,
+                              (char*)t.out + (size_t)r0 * L->view.D * es, (char*)ws + tab_bytes, ws_bytes - tab_bytes,
+                              false, s);
+  }
+  return e;
 }
 
 }  // namespace starkv

@@ -234,4 +234,21 @@ cudaError_t launch_wait_timeout_check(uint32_t* status, unsigned long long limit
   return cudaGetLastError();
 }
 
+// Norm weights (in the layer dtype) as fp32: out[0 .. d) from q, out[d .. 2d) from k (either may be null).
+template <typename T>
+__global__ void k_norms_f32(const T* __restrict__ q, const T* __restrict__ k, int d, float* __restrict__ out) {
+  for (int p = threadIdx.x; p < d; p += blockDim.x) {
+    if (q) out[p] = (float)q[p];
+    if (k) out[d + p] = (float)k[p];
+  }
+}
+
+cudaError_t launch_norms_f32(const void* q, const void* k, int dtype, int d, float* out, cudaStream_t s) {
+  if (dtype == STARKV_F32)
+    k_norms_f32<float><<<1, 128, 0, s>>>((const float*)q, (const float*)k, d, out);
+  else
+    k_norms_f32<__nv_bfloat16><<<1, 128, 0, s>>>((const __nv_bfloat16*)q, (const __nv_bfloat16*)k, d, out);
+  return cudaGetLastError();
+}
+
 }  // namespace starkv

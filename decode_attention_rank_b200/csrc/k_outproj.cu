@@ -184,9 +184,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) k_outproj_tc(OutArgs a) {
 // out[row][n] = sum over the CTAs whose k-range touched output tile n / 128.
 template <typename TO>
 __global__ void k_outproj_reduce(const float* __restrict__ part, int G, int KT, int DT, int slots, int NB, int rows,
-                                 int D, TO* __restrict__ out) {
+                                 int D, const int32_t* __restrict__ n_rows, TO* __restrict__ out) {
   __shared__ long long seg_off[512];
   const int dt = blockIdx.x, row = blockIdx.y;
+  if (n_rows && row >= *n_rows) return;
   const int nt = row / NB, b = row % NB;
   // The CTAs whose unit ranges [begin(c), begin(c + 1)) meet this output
   // tile's k-range [lo, hi): candidates c_lo, c_lo + 1, ... tested one per
@@ -261,7 +262,8 @@ size_t outproj_part_bytes(const starkv_layer* L, int rows) {
 }
 
 cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, const void* y_tiles, int rows,
-                           void* out, bool out_f32, float* part, uint32_t* status, cudaStream_t s, int y_group) {
+                           void* out, bool out_f32, float* part, uint32_t* status, cudaStream_t s, int y_group,
+                           const int32_t* n_rows) {
   const OutGeom g = gemm_geom(n_out, K);
   const int NB = outproj_nb(rows);
   const int ntiles = (rows + NB - 1) / NB;
@@ -291,15 +293,15 @@ cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, con
   }
   if (out_f32)
     k_outproj_reduce<float><<<dim3(g.DT, rows), 128, 0, s>>>(part, g.G, g.KT, g.DT, g.slots, NB, rows, n_valid,
-                                                             (float*)out);
+                                                             n_rows, (float*)out);
   else
     k_outproj_reduce<__nv_bfloat16><<<dim3(g.DT, rows), 128, 0, s>>>(part, g.G, g.KT, g.DT, g.slots, NB, rows,
-                                                                     n_valid, (__nv_bfloat16*)out);
+                                                                     n_valid, n_rows, (__nv_bfloat16*)out);
   return cudaGetLastError();
 }
 
 cudaError_t launch_outproj_tc(const starkv_layer* L, const void* y_tiles, int rows, void* out, float* part,
-                              cudaStream_t s) {
+                              cudaStream_t s, const int32_t* n_rows) {
   if (L->unfused) {
     const LayerView& v = L->view;
     uint8_t* w = (uint8_t*)part;
@@ -309,14 +311,15 @@ cudaError_t launch_outproj_tc(const starkv_layer* L, const void* y_tiles, int ro
     w += unfused_zt_bytes(L, rows);
     float* p2 = (float*)w;
     cudaError_t e = launch_gemm_tc((const uint8_t*)L->Bv_tiles, v.H * v.d, v.wv, v.H * v.d, y_tiles, rows, z, true,
-                                   p2, L->status, s, 1);
+                                   p2, L->status, s, 1, n_rows);
     if (e != cudaSuccess) return e;
     e = launch_pack_rows_tiles_f32(z, rows, v.H * v.d, zt, s);
     if (e != cudaSuccess) return e;
-    return launch_gemm_tc((const uint8_t*)L->Wo_tiles, L->Dp, v.H * v.d, v.D, zt, rows, out, false, p2, L->status, s);
+    return launch_gemm_tc((const uint8_t*)L->Wo_tiles, L->Dp, v.H * v.d, v.D, zt, rows, out, false, p2, L->status, s, 0,
+                          n_rows);
   }
   return launch_gemm_tc((const uint8_t*)L->M_T, L->Dp, L->Kp, L->view.D, y_tiles, rows, out,
-                        L->view.dtype == STARKV_F32, part, L->status, s);
+                        L->view.dtype == STARKV_F32, part, L->status, s, 0, n_rows);
 }
 
 __device__ __forceinline__ float ld_any(const __nv_bfloat16* p, size_t i) { return __bfloat162float(p[i]); }

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(32 * kPlainWarps) k_plain_decode(LayerView v, 
 }  // namespace
 
 bool plain_decode_supported(const LayerView& v) {
-  return v.plain && v.dtype == STARKV_BF16 && v.d == 128 && v.group_q <= kPlainMaxGroup &&
+  return v.plain && !v.quantized && v.dtype == STARKV_BF16 && v.d == 128 && v.group_q <= kPlainMaxGroup &&
          (v.group_q & (v.group_q - 1)) == 0;
 }
 

@@ -52,10 +52,18 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 // cos / sin of every (query, pair) of the chunk, shared by all heads: query i
 // (position q_start + i), pair p: the angle reduced modulo 2 pi in double,
 // then a float sincos.  cs[i][p] = (cos, sin).
-__global__ void k_prefill_qrope(float log2_theta, int q_len, int q_start, float2* __restrict__ cs) {
+__global__ void k_prefill_qrope(float log2_theta, const double* __restrict__ turn, int q_len, int q_start,
+                                float2* __restrict__ cs) {
   const int idx = blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= q_len * 64) return;
   const int i = idx >> 6, p = idx & 63;
+  if (turn) {   // layers of starkv_load_plain: frequencies in turns per position
+    const double t = (double)(q_start + i) * turn[p];
+    float sn, c;
+    sincospif((float)(2.0 * (t - rint(t))), &sn, &c);
+    cs[idx] = make_float2(c, sn);
+    return;
+  }
   const double ang = (double)(q_start + i) * exp2(-(2.0 * p / 128.0) * (double)log2_theta);
   const double two_pi = 6.283185307179586476925286766559;
   float sn, c;
@@ -66,7 +74,9 @@ __global__ void k_prefill_qrope(float log2_theta, int q_len, int q_start, float2
 // Query i of the chunk: RoPE (rotate-half pairs, cos / sin from the table;
 // none when the layer has no RoPE), times softmax scale * log2(e), as row
 // i % 128 of tile [h][i / 128].  Rows past the chunk are zero.  A thread
-// takes (row, 8-pair chunk) items of one head.
+// takes (row, 8-pair chunk) items of one head; the eight threads of a row are
+// neighbours in a warp, so a per-head norm of the query (layers of
+// starkv_load_plain that have one) is a sum over eight lanes.
 __global__ void __launch_bounds__(256) k_prefill_q(LayerView v, const __nv_bfloat16* __restrict__ q, int q_len,
                                                   const float2* __restrict__ cs, int n_qt, uint8_t* __restrict__ Qt) {
   const int qt = blockIdx.x, h = blockIdx.y;
@@ -79,13 +89,30 @@ __global__ void __launch_bounds__(256) k_prefill_q(LayerView v, const __nv_bfloa
     const uint4 rb = i < q_len ? qr[8 + c8] : make_uint4(0, 0, 0, 0);   // elements 64 + 8 c8 ..
     const uint32_t aw[4] = {ra.x, ra.y, ra.z, ra.w}, bw[4] = {rb.x, rb.y, rb.z, rb.w};
     uint32_t lo[4], hi[4];
+    float inv = 1.f;
+    if (v.q_norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a0 = __uint_as_float(aw[k] << 16), a1 = __uint_as_float(aw[k] & 0xFFFF0000u);
+        const float b0 = __uint_as_float(bw[k] << 16), b1 = __uint_as_float(bw[k] & 0xFFFF0000u);
+        ss += a0 * a0 + a1 * a1 + b0 * b0 + b1 * b1;
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      inv = 1.f / sqrtf(ss / 128.f + v.norm_eps);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float re[2], im[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float a = __uint_as_float(x ? aw[k] & 0xFFFF0000u : aw[k] << 16);
-        const float b = __uint_as_float(x ? bw[k] & 0xFFFF0000u : bw[k] << 16);
+        float a = __uint_as_float(x ? aw[k] & 0xFFFF0000u : aw[k] << 16);
+        float b = __uint_as_float(x ? bw[k] & 0xFFFF0000u : bw[k] << 16);
+        if (v.q_norm) {
+          a *= inv * v.q_norm[c8 * 8 + 2 * k + x];
+          b *= inv * v.q_norm[64 + c8 * 8 + 2 * k + x];
+        }
         const float2 t = (v.rope && i < q_len) ? cs[(size_t)i * 64 + c8 * 8 + 2 * k + x] : make_float2(1.f, 0.f);
         re[x] = (a * t.x - b * t.y) * v.scale_log2;
         im[x] = (b * t.x + a * t.y) * v.scale_log2;
@@ -187,7 +214,7 @@ __global__ void k_prefill_zv(LayerView v, const uint8_t* __restrict__ pool, long
 
 // ------------------------------------------------------------------ plain layers: stored K, V as tiles
 // K block of KV head g: [slot][128] bf16 (already rotated); V block:
-// [slot][H_kv 128] bf16.  One CTA per (key tile, KV head); V is transposed
+// [slot][H_kv 128] bf16; or both as 8 / 4-bit codes (kv_bits).  One CTA per (key tile, KV head); V is transposed
 // through shared memory.
 __global__ void __launch_bounds__(256) k_prefill_plain_kv(LayerView v, const uint8_t* __restrict__ pool,
                                                          long long n_pages, const int32_t* __restrict__ pt_row,
@@ -209,6 +236,20 @@ __global__ void __launch_bounds__(256) k_prefill_plain_kv(LayerView v, const uin
         page = 0;
       }
       const uint8_t* base = pool + (size_t)page * v.page_bytes;
+      if (v.kv_bits) {
+        // codes: the values they stand for, fp16 (code * scale stays below 32768 and is rounded once)
+        uint32_t ko[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = c * 8 + 2 * k;
+          ko[k] = pack_half2(latent_value(v, base + kd.block_off, kd, t % kPage, j),
+                             latent_value(v, base + kd.block_off, kd, t % kPage, j + 1));
+          Vs[row][j] = __float2half_rn(latent_value(v, base + vd.block_off, vd, t % kPage, g * 128 + j));
+          Vs[row][j + 1] = __float2half_rn(latent_value(v, base + vd.block_off, vd, t % kPage, g * 128 + j + 1));
+        }
+        *reinterpret_cast<uint4*>(ktile + tile_off(row, c * 8)) = make_uint4(ko[0], ko[1], ko[2], ko[3]);
+        continue;
+      }
       kk = *reinterpret_cast<const uint4*>(base + kd.block_off + ((size_t)(t % kPage) * 128 + c * 8) * 2);
       vv = *reinterpret_cast<const uint4*>(base + vd.block_off + ((size_t)(t % kPage) * v.rv + g * 128 + c * 8) * 2);
     }
@@ -836,7 +877,7 @@ cudaError_t launch_prefill_flash(const starkv_layer* L, const uint8_t* pool, lon
   PrefillWs w = prefill_ws_layout(L, ws, max_T, max_q);
   cudaError_t e;
   if (v.rope) {
-    k_prefill_qrope<<<(q_len * 64 + 255) / 256, 256, 0, s>>>(v.rope_log2_theta, q_len, q_start, w.qcs);
+    k_prefill_qrope<<<(q_len * 64 + 255) / 256, 256, 0, s>>>(v.rope_log2_theta, v.turn, q_len, q_start, w.qcs);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   k_prefill_q<<<dim3(n_qt, v.H), 256, 0, s>>>(v, (const __nv_bfloat16*)q, q_len, w.qcs, n_qt_l, w.Qt);

@@ -79,6 +79,12 @@ struct LayerView {
   float rope_log2_theta;      // log2(theta)
   float scale_log2;           // softmax scale * log2(e)
   long long page_bytes;
+  int kv_bits;                // uncompressed layers: 0 = K and V stored in dtype, 8 or 4 = codes
+  const float* q_norm;        // per-head norm weights [d] (null: none), see starkv_load_plain
+  const float* k_norm;
+  float norm_eps;
+  const double* turn;         // RoPE frequencies in turns per position, theta^(-2p/d) / 2 pi (null without RoPE)
+  int opt;                    // loaded by starkv_load_plain: queries are normed and rotated with `turn`
   const LatentDesc* lat;      // device tables
   const GroupDesc* grp;
   uint32_t* status;
@@ -168,6 +174,8 @@ struct starkv_layer {
   void* Wo_tiles = nullptr;     // fp16 tiles [Dp / 128][H d / 64] of 128 x 64: row n, column k = W_o[k][n]
   void* Bk_tiles = nullptr;     // prefill: per KV head one fp16 128 x 64 tile, row p, column j = B'_k[j][p] (j < r <= 64)
   uint32_t* status = nullptr;
+  float* norms = nullptr;       // [2][d] fp32: q_norm, k_norm (layers of starkv_load_plain that have them)
+  double* turn = nullptr;       // [d / 2]
   // tensor-core score kernel
   bool tc_scores = false;
   std::vector<starkv::ScoreItem> items;
@@ -204,6 +212,8 @@ cudaError_t launch_rotate_rows(const starkv_layer* L, const void* B, int dtype, 
                                cudaStream_t s);
 cudaError_t launch_fold_M(const starkv_layer* L, const float* Bv_rot, const void* W_o, cudaStream_t s);
 
+cudaError_t launch_norms_f32(const void* q, const void* k, int dtype, int d, float* out, cudaStream_t s);
+
 cudaError_t launch_wait_timeout_check(uint32_t* status, unsigned long long limit_ns, cudaStream_t s);
 
 cudaError_t launch_project(const starkv_layer* L, const void* x, int n, float* z, cudaStream_t s);
@@ -216,7 +226,82 @@ struct RowInfo {
   const int32_t* row_seq;   // [rows] sequence of each row, or null = identity
   const int32_t* row_len;   // [rows] visible tokens (decode: seq_lens)
   const int32_t* row_pos;   // [rows] RoPE position of the query, or null = len - 1
+  // rows that are nodes of drafted trees (null row_hist: none): slots below row_hist are visible, slot
+  // row_hist + j is where the row's mask has bit j (no mask: j <= row_node)
+  const int32_t* row_hist = nullptr;
+  const int32_t* row_node = nullptr;
+  const uint32_t* mask = nullptr;      // [rows][mask_words]
+  int mask_words = 0;
+  const int32_t* node_off = nullptr;   // first row of each sequence
+  const int32_t* node_pos = nullptr;   // [rows] RoPE positions of the nodes (their keys', too); null: queries are ready
+  const int32_t* n_rows = nullptr;     // rows in use: output rows from here on are not written
 };
+
+// One sequence's drafted nodes, checked: rows off .. off + cnt - 1 of the call's node arrays, their K and V in slots
+// hist .. hist + cnt - 1.  cnt = 0 (flagged) when they do not fit; off and rows then say which output rows are zero.
+struct TreeSeq {
+  int hist, cnt, off, rows;
+};
+__device__ __forceinline__ TreeSeq tree_seq(const int32_t* hist, const int32_t* node_off, int b, int n_nodes,
+                                            int max_nodes, int cap, uint32_t* status, bool flag) {
+  TreeSeq q{hist[b], 0, node_off[b], 0};
+  const int end = node_off[b + 1];
+  if (q.off < 0 || end < q.off || end > n_nodes) {
+    if (flag) atomicOr(status, STARKV_DEV_BAD_POSITION);
+    q.off = 0;
+    return q;
+  }
+  q.rows = end - q.off;
+  if (q.rows > max_nodes || q.hist < 0 || (long long)q.hist + q.rows > cap) {
+    if (flag) atomicOr(status, STARKV_DEV_BAD_POSITION);
+    return q;
+  }
+  q.cnt = q.rows;
+  return q;
+}
+// Whether node i of a sequence (row `row` of the mask) sees its node j.
+__device__ __forceinline__ bool tree_sees(const uint32_t* mask, int words, int row, int i, int j) {
+  if (mask == nullptr) return j <= i;
+  return (j >> 5) < words && ((mask[(size_t)row * words + (j >> 5)] >> (j & 31)) & 1u);
+}
+
+// K, V and queries of new tokens (k_kv.cu).
+struct KvArgs {
+  LayerView v;
+  uint8_t* pool;               // null: keys go to k_out
+  long long n_pages;
+  const int32_t* pt;
+  int n_seqs, max_pages, n;
+  const int32_t *seq_idx, *slots, *positions;
+  const double* turn;
+  const void *q, *k, *vv;      // rows (null: absent)
+  long long q_ld, k_ld, v_ld;
+  void *q_out, *k_out;
+  long long q_out_ld, k_out_ld;
+  int rotate;
+  int vec;                     // rows, strides and outputs are on 16-byte boundaries
+};
+cudaError_t launch_qkv(const KvArgs& a, bool f32, cudaStream_t s);
+cudaError_t launch_cache_read(const KvArgs& a, void* out, cudaStream_t s);
+cudaError_t launch_accept(const starkv_layer* L, uint8_t* pool, long long n_pages, const int32_t* pt, int max_pages,
+                          int batch, const int32_t* hist, const int32_t* node_off, int n_nodes, int max_nodes,
+                          const int32_t* acc, const int32_t* n_acc, cudaStream_t s);
+// Tree attention (k_tree.cu).
+struct TreeArgs {
+  const uint8_t* pool;
+  long long n_pages;
+  const int32_t* pt;
+  int max_pages, batch;
+  const int32_t *hist, *node_off;
+  int n_nodes, max_nodes;
+  const uint32_t* mask;
+  int mask_words;
+  const void* q;
+  const int32_t* q_pos;        // null: queries are normed and rotated already
+  void* out;
+};
+size_t tree_generic_ws_bytes(const starkv_layer* L, int max_ctx, int n_nodes);
+cudaError_t launch_tree_generic(const starkv_layer* L, const TreeArgs& t, void* ws, size_t ws_bytes, cudaStream_t s);
 cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, long long n_pages,
                                   const int32_t* page_table, int max_pages, int rows, RowInfo ri, int max_len,
                                   const void* q, void* out, void* ws, size_t ws_bytes, bool prefill,
@@ -266,7 +351,8 @@ size_t outproj_part_bytes(const starkv_layer* L, int rows);
 // y_group != 0: a block-diagonal (grouped) product, output tile dt (128 outputs) contracting only
 // y's k-range [dt * K, dt * K + K) (y has n_out / 128 * K columns).
 cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, const void* y_tiles, int rows,
-                           void* out, bool out_f32, float* part, uint32_t* status, cudaStream_t s, int y_group = 0);
+                           void* out, bool out_f32, float* part, uint32_t* status, cudaStream_t s, int y_group = 0,
+                           const int32_t* n_rows = nullptr);
 // Rows of a bf16 matrix as fp16 swizzled tiles of nb rows x 64 columns (nb = 0: the B-tile height for `rows`).
 cudaError_t launch_pack_rows_tiles(const void* x, int rows, int K, void* tiles, cudaStream_t s, int nb = 0);
 cudaError_t launch_pack_rows_tiles_f32(const float* x, int rows, int K, void* tiles, cudaStream_t s, int nb = 0);
@@ -281,7 +367,8 @@ cudaError_t launch_prefill_flash(const starkv_layer* L, const uint8_t* pool, lon
 // as tiles [Dp / 128][H d / 64] (built from the same inputs as M).
 cudaError_t launch_build_unfused(starkv_layer* L, const float* Bv_rot, const void* W_o, cudaStream_t s);
 size_t rows_tiles_bytes(int rows, int K);
+// n_rows (device, may be null): output rows from *n_rows on are not written.
 cudaError_t launch_outproj_tc(const starkv_layer* L, const void* y_tiles, int rows, void* out, float* part,
-                              cudaStream_t s);
+                              cudaStream_t s, const int32_t* n_rows = nullptr);
 
 }  // namespace starkv

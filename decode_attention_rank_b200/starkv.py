@@ -32,7 +32,8 @@ EXPORTED = ["starkv_load_factors", "starkv_free_layer", "starkv_layer_get_info",
             "starkv_cache_init", "starkv_append", "starkv_append_workspace_bytes", "starkv_decode_attn",
             "starkv_prefill_attn", "starkv_workspace_bytes", "starkv_sync_status", "starkv_status_string",
             "starkv_last_error", "starkv_version", "starkv_decode_attn_noalloc", "starkv_set_decode_path",
-            "starkv_check_wait_timeout"]
+            "starkv_check_wait_timeout", "starkv_load_plain", "starkv_qk_norm_rope", "starkv_append_qkv",
+            "starkv_cache_read", "starkv_tree_attn", "starkv_tree_workspace_bytes", "starkv_tree_accept"]
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -81,6 +82,18 @@ _lib.starkv_set_decode_path.argtypes = [_vp, ctypes.c_int]
 _lib.starkv_check_wait_timeout.argtypes = [_vp, ctypes.c_uint32, _vp]
 _lib.starkv_profile_decode.argtypes = [_vp, ctypes.c_int]
 _lib.starkv_decode_phase_ms.argtypes = [_vp, ctypes.POINTER(ctypes.c_float), ctypes.c_int]
+_int = ctypes.c_int
+_lib.starkv_load_plain.argtypes = [ctypes.POINTER(_Config), _int, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp,
+                                   ctypes.POINTER(_vp)]
+_lib.starkv_qk_norm_rope.argtypes = [_vp, _int, _i32p, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+_lib.starkv_append_qkv.argtypes = [_vp, _vp, _i64, _i32p, _int, _int, _int, _i32p, _i32p, _i32p, _vp, _i64, _vp, _i64,
+                                   _vp, _i64, _vp, _i64, _vp]
+_lib.starkv_cache_read.argtypes = [_vp, _vp, _i64, _i32p, _int, _int, _int, _i32p, _i32p, _vp, _vp]
+_lib.starkv_tree_attn.argtypes = [_vp, _vp, _i64, _i32p, _int, _int, _i32p, _i32p, _int, _int, _vp, _int, _vp, _i32p,
+                                  _vp, _vp, _sz, _vp]
+_lib.starkv_tree_workspace_bytes.argtypes = [_vp, _int, _int, _int, _int]
+_lib.starkv_tree_workspace_bytes.restype = _sz
+_lib.starkv_tree_accept.argtypes = [_vp, _vp, _i64, _i32p, _int, _int, _i32p, _i32p, _int, _int, _i32p, _i32p, _vp]
 N_PHASES = 4   # query preparation + scores, joint values, run merge, output projection
 _lib.starkv_version.argtypes = []
 _lib.starkv_version.restype = ctypes.c_char_p
@@ -105,6 +118,25 @@ def version() -> str:
 def _ptr(t) -> int:
     if t is None:
         return None
+    return t.data_ptr()
+
+
+def _rows(t, n: int, width: int, name: str):
+    """Pointer and row stride of n rows of `width` elements ([n, width] or [n, heads, d]; rows may be strided)."""
+    if t is None:
+        return None, 0
+    inner = t.dim() == 2 or (t.dim() == 3 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]))
+    if not inner or t.shape[0] != n or t.numel() != n * width or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be [{n}, {width}] with contiguous rows, got {list(t.shape)}")
+    return t.data_ptr(), t.stride(0) if n > 1 else width
+
+
+def _ints(t, n: int, name: str):
+    """Pointer of a contiguous int32 array of n elements."""
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.is_floating_point() or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 array of {n} elements")
     return t.data_ptr()
 
 
@@ -226,6 +258,89 @@ class Layer:
                                         _ptr(workspace), workspace.numel() * workspace.element_size(),
                                         _stream(stream)), "starkv_prefill_attn")
 
+    # ---- serving an uncompressed layer, and speculative decoding (see include/starkv.h)
+
+    def _same_dtype(self, **tensors) -> None:
+        want = "torch.float32" if self.cfg.dtype == "f32" else "torch.bfloat16"
+        for name, t in tensors.items():
+            if t is not None and str(t.dtype) != want:
+                raise ValueError(f"{name} must have the layer's dtype ({want}), got {t.dtype}")
+
+    def qk_norm_rope(self, q, k, positions, q_out, k_out, stream=None) -> None:
+        """Per-head norm and rotation of queries and keys (either pair may be None)."""
+        self._same_dtype(q=q, k=k, q_out=q_out, k_out=k_out)
+        some = q if q is not None else k
+        n = int(some.shape[0]) if some is not None else 0
+        wq, wk = self.cfg.n_heads * self.cfg.head_dim, self.cfg.n_kv_heads * self.cfg.head_dim
+        (qp, ql), (kp, kl) = _rows(q, n, wq, "q"), _rows(k, n, wk, "k")
+        (qo, qol), (ko, kol) = _rows(q_out, n, wq, "q_out"), _rows(k_out, n, wk, "k_out")
+        _check(_lib.starkv_qk_norm_rope(self._h, n, _ints(positions, n, "positions"), qp, ql, kp, kl, qo, qol, ko, kol,
+                                        _stream(stream)), "starkv_qk_norm_rope")
+
+    def append_qkv(self, pool, n_pages: int, page_table, seq_idx, slots, q, k, v, q_out=None, positions=None,
+                   stream=None) -> None:
+        """Norm, rotation and storing (or quantising) of new tokens' projections in one pass."""
+        self._same_dtype(q=q, k=k, v=v, q_out=q_out)
+        n = int(seq_idx.numel())
+        wq, wk = self.cfg.n_heads * self.cfg.head_dim, self.cfg.n_kv_heads * self.cfg.head_dim
+        (qp, ql), (kp, kl), (vp, vl) = _rows(q, n, wq, "q"), _rows(k, n, wk, "k"), _rows(v, n, wk, "v")
+        qo, qol = _rows(q_out, n, wq, "q_out")
+        _check(_lib.starkv_append_qkv(self._h, _ptr(pool), n_pages, _ints(page_table, page_table.numel(), "page_table"),
+                                      int(page_table.shape[0]), int(page_table.shape[1]), n,
+                                      _ints(seq_idx, n, "seq_idx"), _ints(slots, n, "slots"),
+                                      _ints(positions, n, "positions"), qp, ql, kp, kl, vp, vl, qo, qol,
+                                      _stream(stream)), "starkv_append_qkv")
+
+    def cache_read(self, pool, n_pages: int, page_table, seq_idx, slots, out, stream=None) -> None:
+        """Cached tokens as dense rows [n, latent_total]."""
+        self._same_dtype(out=out)
+        n = int(seq_idx.numel())
+        op, ol = _rows(out, n, self.latent_total, "out")
+        if n and ol != self.latent_total:
+            raise ValueError("out must be contiguous")
+        _check(_lib.starkv_cache_read(self._h, _ptr(pool), n_pages, _ints(page_table, page_table.numel(), "page_table"),
+                                      int(page_table.shape[0]), int(page_table.shape[1]), n,
+                                      _ints(seq_idx, n, "seq_idx"), _ints(slots, n, "slots"), op, _stream(stream)),
+               "starkv_cache_read")
+
+    def tree_workspace_bytes(self, batch: int, max_ctx: int, n_nodes: int, max_nodes: int) -> int:
+        return _lib.starkv_tree_workspace_bytes(self._h, batch, max_ctx, n_nodes, max_nodes)
+
+    def tree_attn(self, pool, n_pages: int, page_table, hist, node_off, q, out, workspace, max_nodes: int, mask=None,
+                  q_pos=None, stream=None) -> None:
+        """Attention of drafted nodes over the cache: mask int32 [n_nodes, words] (bits), None = a chain."""
+        self._same_dtype(q=q, out=out)
+        batch, n = int(hist.numel()), int(q.shape[0])
+        words = 0
+        if mask is not None:
+            if mask.dim() != 2 or mask.shape[0] != n:
+                raise ValueError(f"mask must be [{n}, words]")
+            words = int(mask.shape[1])
+        qp, ql = _rows(q, n, self.cfg.n_heads * self.cfg.head_dim, "q")
+        op, ol = _rows(out, n, self.cfg.hidden, "out")
+        if n and (ql != self.cfg.n_heads * self.cfg.head_dim or ol != self.cfg.hidden):
+            raise ValueError("q and out must be contiguous")
+        if page_table.shape[0] < batch:
+            raise ValueError(f"page_table must have at least {batch} rows")
+        _check(_lib.starkv_tree_attn(self._h, _ptr(pool), n_pages, _ints(page_table, page_table.numel(), "page_table"),
+                                     int(page_table.shape[1]), batch, _ints(hist, batch, "hist"),
+                                     _ints(node_off, batch + 1, "node_off"), n, max_nodes,
+                                     _ints(mask, n * words, "mask"), words, qp, _ints(q_pos, n, "q_pos"), op,
+                                     _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+               "starkv_tree_attn")
+
+    def tree_accept(self, pool, n_pages: int, page_table, hist, node_off, acc, n_acc, max_nodes: int,
+                    stream=None) -> None:
+        """Move the accepted nodes' slots to the front and clear the other nodes' slots."""
+        batch, n = int(hist.numel()), int(acc.numel())
+        if page_table.shape[0] < batch:
+            raise ValueError(f"page_table must have at least {batch} rows")
+        _check(_lib.starkv_tree_accept(self._h, _ptr(pool), n_pages,
+                                       _ints(page_table, page_table.numel(), "page_table"), int(page_table.shape[1]),
+                                       batch, _ints(hist, batch, "hist"), _ints(node_off, batch + 1, "node_off"), n,
+                                       max_nodes, _ints(acc, n, "acc"), _ints(n_acc, batch, "n_acc"), _stream(stream)),
+               "starkv_tree_accept")
+
     def set_decode_path(self, path: int) -> None:
         """0 automatic, 1 CUDA-core kernels, 2 tensor-core scores + CUDA-core values (diagnostics)."""
         _check(_lib.starkv_set_decode_path(self._h, path), "starkv_set_decode_path")
@@ -264,6 +379,21 @@ def load_factors(cfg: LayerConfig, A_k, B_k, A_v, B_v, W_o, stream=None) -> Laye
     h = _vp()
     _check(_lib.starkv_load_factors(ctypes.byref(c), _ptr(A_k), _ptr(B_k), _ptr(A_v), _ptr(B_v), _ptr(W_o),
                                     _stream(stream), ctypes.byref(h)), "starkv_load_factors")
+    del keep
+    return Layer(h.value, cfg)
+
+
+def load_plain(cfg: LayerConfig, W_k, W_v, W_o, kv_bits: int = 0, q_norm=None, k_norm=None, norm_eps: float = 1e-6,
+               stream=None) -> Layer:
+    """Load an uncompressed layer with a quantised cache (kv_bits 8 or 4) and per-head query / key norms."""
+    want = "torch.float32" if cfg.dtype == "f32" else "torch.bfloat16"
+    for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if t is not None and (str(t.dtype) != want or t.numel() != cfg.head_dim or not t.is_contiguous()):
+            raise ValueError(f"{name} must hold {cfg.head_dim} elements of the layer's dtype ({want})")
+    c, keep = cfg._c()
+    h = _vp()
+    _check(_lib.starkv_load_plain(ctypes.byref(c), kv_bits, _ptr(q_norm), _ptr(k_norm), norm_eps, _ptr(W_k), _ptr(W_v),
+                                  _ptr(W_o), _stream(stream), ctypes.byref(h)), "starkv_load_plain")
     del keep
     return Layer(h.value, cfg)
 

@@ -294,6 +294,120 @@ STARKV_API starkv_status starkv_decode_attn_noalloc(const starkv_layer* layer, c
                                                     const int32_t* seq_lens, const int32_t* q_pos, const void* q,
                                                     void* out, starkv_stream_t stream);
 
+/*
+ * ---- Serving an uncompressed layer, and speculative decoding on any layer ----
+ *
+ * Load an uncompressed layer (cfg->plain = 1) with what starkv_load_factors
+ * does not take: a quantised cache, and per-head norms of queries and keys.
+ *   kv_bits: 0 = K and V stored in dtype; 8 or 4 = codes with one fp16 scale
+ *     per (token, KV head, 32 channels): scale = amax / (2^(bits-1) - 1) in
+ *     fp32, rounded up to fp16, code = round-half-even(x / scale) + 2^(bits-1).
+ *     Page: per KV head the key block, then one value block of H_kv * d
+ *     channels; a block is its scales [group][slot] fp16, then per group
+ *     [slot][32 codes], LSB first (head_dim 64, 128 or 256).  A group whose
+ *     largest magnitude is above 32768, an infinity or a NaN is stored as
+ *     zeros and sets STARKV_DEV_SCALE_OVF.
+ *   q_norm, k_norm: device [d] weights in dtype, or NULL for no norm:
+ *     x * rsqrt(mean(x^2) + norm_eps) * w for each head's d channels, before
+ *     the rotation.  norm_eps in [0, 1].
+ * Everything else is as in starkv_load_factors.  The rotation is evaluated
+ * with the angle in 64 bits.  starkv_append (from hidden states; input
+ * latents are K and V after norm and rotation), starkv_decode_attn and
+ * starkv_prefill_attn work on such a layer and apply its norms to q.
+ */
+STARKV_API starkv_status starkv_load_plain(const starkv_layer_config* cfg, int kv_bits, const void* q_norm,
+                                           const void* k_norm, float norm_eps, const void* W_k, const void* W_v,
+                                           const void* W_o, starkv_stream_t stream, starkv_layer** out);
+
+/*
+ * Norm (where the layer has weights) and rotation of the queries and keys of
+ * n_tokens tokens, one pass.  Layers of starkv_load_plain.
+ *   positions: int32 [n_tokens] (may be NULL when cfg.rope = 0).
+ *   q: row i at q + i * q_ld, H * d channels in dtype; k: H_kv * d.  The row
+ *     strides are in elements, so a fused projection's rows can be given as they are.
+ *     Either of q and k may be NULL.  q_out, k_out: likewise; a tensor may be its own output.
+ */
+STARKV_API starkv_status starkv_qk_norm_rope(const starkv_layer* layer, int n_tokens, const int32_t* positions,
+                                             const void* q, int64_t q_ld, const void* k, int64_t k_ld, void* q_out,
+                                             int64_t q_out_ld, void* k_out, int64_t k_out_ld, starkv_stream_t stream);
+
+/*
+ * The same for new tokens, with K (normed, rotated) and V stored or quantised
+ * into their slots in that pass.  Layers of starkv_load_plain.
+ *   slots: int32 [n_tokens], the token's slot in its sequence (page
+ *     page_table[b][slot / 16], slot % 16); positions: its rotation position,
+ *     or NULL = slots (drafted tokens of one depth share a position).
+ *   q (may be NULL): normed and rotated into q_out, for a starkv_tree_attn with q_pos = NULL.
+ * A slot may hold a token already: it is overwritten.  The tokens of one call
+ * must go to distinct slots.  A slot or page outside its range sets the status
+ * word and that token is not stored.  With kv_bits the rows of q, k, v and
+ * q_out must start on 16-byte boundaries.
+ */
+STARKV_API starkv_status starkv_append_qkv(const starkv_layer* layer, void* pool, int64_t n_pages,
+                                           const int32_t* page_table, int n_seqs, int max_pages, int n_tokens,
+                                           const int32_t* seq_idx, const int32_t* slots, const int32_t* positions,
+                                           const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v,
+                                           int64_t v_ld, void* q_out, int64_t q_out_ld, starkv_stream_t stream);
+
+/*
+ * Cached tokens as dense rows: out [n_tokens][latent_total] in dtype, latents
+ * in order (uncompressed layers: K of every KV head as stored, then V).
+ * Codes are returned as the values they stand for.  Any layer.  A token whose
+ * slot or page is outside its range gives a zero row and sets the status word.
+ */
+STARKV_API starkv_status starkv_cache_read(const starkv_layer* layer, const void* pool, int64_t n_pages,
+                                           const int32_t* page_table, int n_seqs, int max_pages, int n_tokens,
+                                           const int32_t* seq_idx, const int32_t* slots, void* out,
+                                           starkv_stream_t stream);
+
+/*
+ * Attention of drafted tokens over the cache, through the output projection
+ * like starkv_decode_attn: the verification step of speculative decoding.
+ * Sequence b has hist[b] verified tokens in slots [0, hist[b]) and
+ * node_off[b + 1] - node_off[b] drafted nodes, whose K and V are already in
+ * slots hist[b], hist[b] + 1, ...  Every node sees all of [0, hist[b]) and the
+ * nodes its mask names.  Any layer.
+ *   hist: int32 [batch].  node_off: int32 [batch + 1], increasing, within [0, n_nodes]; a sequence may have none.
+ *   mask: uint32 [n_nodes][mask_words], bit j of row i = node i sees node j of
+ *     its own sequence (its own bit included, where it is to see itself);
+ *     mask_words * 32 >= max_nodes.  NULL: node i sees nodes 0 .. i (a chain;
+ *     with one node, a decode step).  A node that sees nothing gives a zero row.
+ *   max_nodes: upper bound of the nodes of one sequence, 1 .. 1024.
+ *   q: [n_nodes][H][d] in dtype.  q_pos: int32 [n_nodes] rotation positions of
+ *     raw queries, or NULL: the queries are normed and rotated already.  Latent
+ *     layers with RoPE need q_pos, and rotate the nodes' keys at q_pos too.
+ *   out: [n_nodes][D] in dtype.  Rows outside [node_off[0], node_off[batch]) are left as they are.
+ *   workspace: starkv_tree_workspace_bytes(layer, batch, max_pages * 16, n_nodes, max_nodes) bytes.
+ * A sequence with more than max_nodes nodes, or whose slots leave the page
+ * table, sets STARKV_DEV_BAD_POSITION and its rows are zero.  The call reads
+ * hist, node_off and mask on the device only, so it can be captured and
+ * replayed with other contents.
+ */
+STARKV_API starkv_status starkv_tree_attn(const starkv_layer* layer, const void* pool, int64_t n_pages,
+                                          const int32_t* page_table, int max_pages, int batch, const int32_t* hist,
+                                          const int32_t* node_off, int n_nodes, int max_nodes, const uint32_t* mask,
+                                          int mask_words, const void* q, const int32_t* q_pos, void* out,
+                                          void* workspace, size_t ws_bytes, starkv_stream_t stream);
+
+/* Workspace bytes of a starkv_tree_attn call; 0 for a NULL layer or sizes out of range. */
+STARKV_API size_t starkv_tree_workspace_bytes(const starkv_layer* layer, int batch, int max_ctx, int n_nodes,
+                                              int max_nodes);
+
+/*
+ * Keep the accepted path of every sequence's nodes: slot hist[b] + acc[k] of
+ * sequence b moves to hist[b] + k for k < n_acc[b], and the slots
+ * hist[b] + n_acc[b] .. of its other nodes are cleared, so that appends of any
+ * kind can fill them again.  Any layer.
+ *   acc: int32 [n_nodes], sequence b's accepted node numbers at acc[node_off[b]] ..,
+ *     strictly increasing; entries from n_acc[b] on are not read.  n_acc: int32 [batch], 0 .. the sequence's nodes.
+ * A sequence whose path is not of that form sets STARKV_DEV_BAD_POSITION and
+ * is left as it was.
+ */
+STARKV_API starkv_status starkv_tree_accept(const starkv_layer* layer, void* pool, int64_t n_pages,
+                                            const int32_t* page_table, int max_pages, int batch, const int32_t* hist,
+                                            const int32_t* node_off, int n_nodes, int max_nodes, const int32_t* acc,
+                                            const int32_t* n_acc, starkv_stream_t stream);
+
 STARKV_API const char* starkv_status_string(starkv_status s);
 
 /* Message of the last host-side error on this thread ("" if none). */
