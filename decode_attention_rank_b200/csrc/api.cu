@@ -564,6 +564,11 @@ size_t prefill_tc_ws_bytes(const starkv_layer* L, long long rows, int max_pages)
          decode_tc_ws_bytes(L, nb, max_pages * kPage);
 }
 
+// Decodes of a quantised uncompressed cache run as a tree of one node per sequence; path 1 keeps the CUDA-core kernels.
+bool decode_by_tree(const starkv_layer* L) {
+  return L->view.kv_bits != 0 && tree_mma_supported(L->view) && L->decode_path != 1;
+}
+
 }  // namespace
 }  // namespace starkv
 
@@ -572,6 +577,7 @@ size_t starkv_workspace_bytes(const starkv_layer* L, int batch, int max_ctx, int
   if (max_q < 1) max_q = 1;
   max_ctx = std::max(max_ctx, 1);
   size_t need = decode_generic_ws_bytes(L, batch, max_ctx, false);
+  if (decode_by_tree(L)) need = std::max(need, tree_mma_ws_bytes(L, batch, batch, 1));
   if (L->tc_scores) need += scores_tc_ws_bytes(L, batch, max_ctx);
   if (L->tc_values) need = std::max(need, decode_tc_ws_bytes(L, batch, max_ctx));
   if (max_q > 1) {
@@ -606,9 +612,16 @@ starkv_status starkv_decode_attn(const starkv_layer* L, const void* pool, int64_
   size_t need = decode_generic_ws_bytes(L, batch, max_len, false) +
                 (L->tc_scores ? scores_tc_ws_bytes(L, batch, max_len) : 0);
   if (use_tc_all) need = decode_tc_ws_bytes(L, batch, max_len);
+  if (decode_by_tree(L)) need = tree_mma_ws_bytes(L, batch, batch, 1);
   if (workspace == nullptr || ws_bytes < need) {
     set_error("decode workspace too small: need " + std::to_string(need) + " bytes");
     return STARKV_ERR_WORKSPACE;
+  }
+  if (decode_by_tree(L)) {
+    const TreeArgs t{(const uint8_t*)pool, n_pages, page_table, max_pages, batch, nullptr, nullptr, batch, 1, nullptr, 0,
+                     q, q_pos, out, 1, seq_lens};
+    CUDA_TRY(launch_tree_mma(L, t, workspace, ws_bytes, (cudaStream_t)stream));
+    return STARKV_OK;
   }
   if (use_tc_all) {
     CUDA_TRY(launch_decode_tc(L, (const uint8_t*)pool, n_pages, page_table, max_pages, batch, seq_lens, q_pos, q, out,

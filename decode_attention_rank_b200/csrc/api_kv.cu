@@ -176,6 +176,7 @@ starkv_status starkv_cache_read(const starkv_layer* L, const void* pool, int64_t
 
 size_t starkv_tree_workspace_bytes(const starkv_layer* L, int batch, int max_ctx, int n_nodes, int max_nodes) {
   if (!L || batch <= 0 || n_nodes <= 0 || max_nodes <= 0 || max_nodes > kMaxNodes) return 0;
+  if (tree_mma_supported(L->view)) return tree_mma_ws_bytes(L, batch, n_nodes, max_nodes);
   return tree_generic_ws_bytes(L, std::max(max_ctx, 1), n_nodes);
 }
 
@@ -207,8 +208,11 @@ starkv_status starkv_tree_attn(const starkv_layer* L, const void* pool, int64_t 
     return STARKV_ERR_WORKSPACE;
   }
   TreeArgs t{(const uint8_t*)pool, n_pages, page_table, max_pages, batch, hist, node_off, n_nodes, max_nodes,
-             mask, mask_words, q, q_pos, out};
-  CUDA_TRY(launch_tree_generic(L, t, workspace, ws_bytes, (cudaStream_t)stream));
+             mask, mask_words, q, q_pos, out, q_pos != nullptr, nullptr};
+  if (tree_mma_supported(v))
+    CUDA_TRY(launch_tree_mma(L, t, workspace, ws_bytes, (cudaStream_t)stream));
+  else
+    CUDA_TRY(launch_tree_generic(L, t, workspace, ws_bytes, (cudaStream_t)stream));
   return STARKV_OK;
 }
 

@@ -174,7 +174,17 @@ __global__ void k_pack_groups(LayerView v, const int* __restrict__ grp_lat, int 
   float amax = lane < gd.n ? fabsf(x) : 0.f;
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const int qmax = (1 << (gd.bits - 1)) - 1;
-  const float s32 = __fdiv_rn(amax, (float)qmax);
+  // uncompressed layers' codes (kv_bits): the scale of starkv_append_qkv, a product with the rounded 1 / qmax, and a
+  // group that has no code stored as zeros
+  float s32 = v.kv_bits ? __fmul_rn(amax, __fdiv_rn(1.f, (float)qmax)) : __fdiv_rn(amax, (float)qmax);
+  if (v.kv_bits) {
+    const bool bad = __any_sync(0xffffffffu, !(fabsf(x) <= kKvMax));
+    if (bad) {
+      if (lane == 0) atomicOr(v.status, kScaleOvf);
+      s32 = 0.f;
+      x = 0.f;
+    }
+  }
   if (!(s32 <= 65504.f)) {
     if (lane == 0) atomicOr(v.status, kScaleOvf);
     return;

@@ -464,7 +464,10 @@ __global__ void k_tree_rows(LayerView v, const int32_t* __restrict__ hist, const
   if (r % kTreeRows == 0)
     n_rows[r / kTreeRows] = min(max(min(node_off[batch], n_nodes) - r, 0), kTreeRows);
   int32_t seq = 0, len = 0, h = 0, node = 0;
-  for (int b = 0; b < batch; ++b) {
+  bool back = false;   // a node_off that decreases: every row is zero
+  for (int b = 0; b < batch; ++b) back = back || node_off[b + 1] < node_off[b];
+  if (back && r == 0) atomicOr(v.status, kBadPos);
+  for (int b = 0; b < batch && !back; ++b) {
     if (r < node_off[b] || r >= node_off[b + 1]) continue;
     const TreeSeq q = tree_seq(hist, node_off, b, n_nodes, max_nodes, cap, v.status, r == node_off[b]);
     seq = b;

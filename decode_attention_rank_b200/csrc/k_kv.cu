@@ -8,8 +8,8 @@
 //   x'  = x * rsqrt(mean(x^2) + eps) * w                       (only where the layer has weights)
 //   y[p] = x'[p] cos a - x'[p + half] sin a,  y[p + half] = x'[p + half] cos a + x'[p] sin a,
 //   a = position * theta^(-2p/d), reduced in 64 bits (as turns: the fraction of position * f / 2 pi)
-// Quantiser (kv_bits b, groups of 32 channels, qmax = 2^(b-1) - 1): scale = amax / qmax in fp32, rounded up to
-// fp16; code = rne(x / scale) + 2^(b-1), the fp32 division.
+// Quantiser (kv_bits b, groups of 32 channels, qmax = 2^(b-1) - 1): scale = amax * fl(1 / qmax) in fp32, rounded
+// up to fp16; code = rne(x / scale) + 2^(b-1), the fp32 division.
 #include <float.h>
 
 #include "starkv_internal.cuh"
@@ -19,7 +19,6 @@ namespace starkv {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr float kKvMax = 32768.f;   // largest magnitude a quantised page holds: code * scale stays inside fp16
 
 template <typename T>
 struct Vec;
@@ -139,7 +138,7 @@ __device__ __forceinline__ void quant_store(const float* x, uint8_t* blk, int sc
   for (int o = GL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (!live) return;
   const bool fits = amax <= kKvMax;
-  const float s32 = fits ? __fdiv_rn(amax, (float)QM) : 0.f;
+  const float s32 = fits ? __fmul_rn(amax, 1.f / (float)QM) : 0.f;
   const __half s16 = __float2half_ru(s32);
   const float sf = __half2float(s16);
   uint32_t u[V];

@@ -62,6 +62,9 @@ constexpr uint32_t kBadPos = STARKV_DEV_BAD_POSITION;
 constexpr uint32_t kScaleOvf = STARKV_DEV_SCALE_OVF;
 constexpr uint32_t kTimeout = STARKV_DEV_TIMEOUT;
 
+// Largest magnitude that an uncompressed layer's codes hold: code * scale stays inside fp16.
+constexpr float kKvMax = 32768.f;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Everything a kernel needs to read or write one layer's pages.
@@ -297,9 +300,14 @@ struct TreeArgs {
   const uint32_t* mask;
   int mask_words;
   const void* q;
-  const int32_t* q_pos;        // null: queries are normed and rotated already
+  const int32_t* q_pos;
   void* out;
+  int raw;                     // queries are to be normed and rotated (at q_pos; decode: at lens - 1 when q_pos is null)
+  const int32_t* lens;         // decode: one query per sequence over lens[b] tokens (hist and node_off are null)
 };
+bool tree_mma_supported(const LayerView& v);
+size_t tree_mma_ws_bytes(const starkv_layer* L, int batch, int n_nodes, int max_nodes);
+cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, size_t ws_bytes, cudaStream_t s);
 size_t tree_generic_ws_bytes(const starkv_layer* L, int max_ctx, int n_nodes);
 cudaError_t launch_tree_generic(const starkv_layer* L, const TreeArgs& t, void* ws, size_t ws_bytes, cudaStream_t s);
 cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, long long n_pages,

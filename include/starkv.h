@@ -300,7 +300,7 @@ STARKV_API starkv_status starkv_decode_attn_noalloc(const starkv_layer* layer, c
  * Load an uncompressed layer (cfg->plain = 1) with what starkv_load_factors
  * does not take: a quantised cache, and per-head norms of queries and keys.
  *   kv_bits: 0 = K and V stored in dtype; 8 or 4 = codes with one fp16 scale
- *     per (token, KV head, 32 channels): scale = amax / (2^(bits-1) - 1) in
+ *     per (token, KV head, 32 channels): scale = amax * (1 / (2^(bits-1) - 1)) in
  *     fp32, rounded up to fp16, code = round-half-even(x / scale) + 2^(bits-1).
  *     Page: per KV head the key block, then one value block of H_kv * d
  *     channels; a block is its scales [group][slot] fp16, then per group
@@ -367,7 +367,7 @@ STARKV_API starkv_status starkv_cache_read(const starkv_layer* layer, const void
  * node_off[b + 1] - node_off[b] drafted nodes, whose K and V are already in
  * slots hist[b], hist[b] + 1, ...  Every node sees all of [0, hist[b]) and the
  * nodes its mask names.  Any layer.
- *   hist: int32 [batch].  node_off: int32 [batch + 1], increasing, within [0, n_nodes]; a sequence may have none.
+ *   hist: int32 [batch].  node_off: int32 [batch + 1], from 0 on, not decreasing, up to n_nodes; a sequence may have no nodes.
  *   mask: uint32 [n_nodes][mask_words], bit j of row i = node i sees node j of
  *     its own sequence (its own bit included, where it is to see itself);
  *     mask_words * 32 >= max_nodes.  NULL: node i sees nodes 0 .. i (a chain;
@@ -376,10 +376,11 @@ STARKV_API starkv_status starkv_cache_read(const starkv_layer* layer, const void
  *   q: [n_nodes][H][d] in dtype.  q_pos: int32 [n_nodes] rotation positions of
  *     raw queries, or NULL: the queries are normed and rotated already.  Latent
  *     layers with RoPE need q_pos, and rotate the nodes' keys at q_pos too.
- *   out: [n_nodes][D] in dtype.  Rows outside [node_off[0], node_off[batch]) are left as they are.
+ *   out: [n_nodes][D] in dtype.  Rows from node_off[batch] on are left as they are.
  *   workspace: starkv_tree_workspace_bytes(layer, batch, max_pages * 16, n_nodes, max_nodes) bytes.
- * A sequence with more than max_nodes nodes, or whose slots leave the page
- * table, sets STARKV_DEV_BAD_POSITION and its rows are zero.  The call reads
+ * A sequence with more than max_nodes nodes, or whose rows or slots leave
+ * [0, n_nodes) or the page table, sets STARKV_DEV_BAD_POSITION and its rows are
+ * zero; a node_off that decreases does so for every row.  The call reads
  * hist, node_off and mask on the device only, so it can be captured and
  * replayed with other contents.
  */

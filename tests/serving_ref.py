@@ -24,7 +24,7 @@ def quantise(x, bits):
     """x [..., 32 m] float64 (first rounded to fp32) -> (scales fp16 [..., m], codes int64 [..., m, 32])."""
     q = 2 ** (bits - 1) - 1
     g = x.to(torch.float32).reshape(*x.shape[:-1], -1, 32)
-    s32 = g.abs().amax(-1) / torch.tensor(float(q), dtype=torch.float32)
+    s32 = g.abs().amax(-1) * (torch.tensor(1.0) / torch.tensor(float(q)))
     s = s32.to(torch.float16)
     up = (s.view(torch.int16) + 1).view(torch.float16)
     s = torch.where(s.to(torch.float32) < s32, up, s)

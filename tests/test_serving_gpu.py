@@ -255,6 +255,28 @@ def test_append_values_without_a_code(bits, bad):
     assert torch.equal(out.cpu(), R_) and p.L.sync_status() == 4
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_append_of_latents_packs_the_same(bits):
+    """starkv_append of K and V rows writes the bytes of starkv_append_qkv, scales at the fp16 borders among them."""
+    p = Plain(2, 1, 128, bits, "f32", norm=False, rope=False)
+    n = 200
+    a, b = p.cache([n]), p.cache([n])
+    x = torch.randn(n, 256)
+    x[:, 5] = torch.arange(n) * (2 ** (bits - 1) - 1) / 16.0           # amax / qmax is an fp16 number
+    x[7, 200] = float("nan")
+    x = x.cuda()
+    slots = i32(torch.arange(n))
+    p.L.append_qkv(a.upload(), a.n_pages, a.pt_d, i32([0] * n), slots, None, x[:, :128], x[:, 128:])
+    p.L.append(b.upload(), b.n_pages, b.pt_d, i32([0] * n), slots, x, True)
+    assert p.L.sync_status() == 4
+    assert torch.equal(a.download(), b.download())
+    K, V = x[:, :128].cpu().to(torch.float64), x[:, 128:].cpu().to(torch.float64)
+    V[7, 64:96] = 0
+    R.put(a.pages, a.pt[0, torch.arange(n) // 16], torch.arange(n) % 16, K.reshape(n, 1, 128), V.reshape(n, 1, 128),
+          bits, p.dt)
+    assert torch.equal(a.download(), a.pages)
+
+
 @pytest.mark.parametrize("quantized", [False, True])
 def test_cache_read_latent_layer(quantized):
     spec = gen.config_spec(3, quantized=quantized)
@@ -328,7 +350,7 @@ TREES = [
     # H, hkv, hist, counts
     (4, 4, [0], [1]), (4, 4, [1], [1]), (4, 2, [15, 0, 16], [1, 1, 1]), (8, 1, [333], [7]),
     (4, 4, [31, 700, 0, 5], [16, 3, 9, 0]), (4, 1, [130, 1025], [33, 64]), (16, 2, [40, 250], [24, 13]),
-    (2, 2, [257], [100]), (32, 8, [77, 5], [24, 31]), (8, 8, [2000, 1999], [5, 8])]
+    (2, 2, [257], [100]), (4, 2, [9, 9, 9] * 23, [1, 2, 0] * 23), (32, 8, [77, 5], [24, 31]), (8, 8, [2000, 1999], [5, 8])]
 
 
 @pytest.mark.parametrize("bits", [0, 8, 4])
@@ -416,6 +438,48 @@ def test_tree_bad_counts_and_pages(bits):
     out = args["out"].to(torch.float64).cpu()
     assert p.L.sync_status() == 1
     check_tree(torch.cat((out[:4], out[9:])), torch.cat((want[:4], want[9:])), "bf16")
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+def test_tree_node_offsets_that_go_back(bits):
+    """Offsets that decrease are flagged and every row is zero; a sequence outside the call's rows leaves the others."""
+    p = Plain(4, 2, 128, bits)
+    got, want, c, args = run_tree(p, [20, 20, 20], [4, 5, 3], None)
+    for off in ([0, 4, 0, 3], [0, 12, 4, 12], [0, 4, 4, 40], [-5, 4, 9, 12], [0, 4, 2 ** 31 - 1, -2 ** 31]):
+        args["node_off"] = i32(off)
+        args["max_nodes"] = 12
+        ws = torch.empty(p.L.tree_workspace_bytes(3, c.pt.shape[1] * 16, 12, 12), dtype=torch.uint8, device="cuda")
+        p.L.tree_attn(**dict(args, workspace=ws))
+        assert p.L.sync_status() == 2, off
+        if off == [0, 4, 4, 40]:
+            check_tree(args["out"][:4].to(torch.float64).cpu(), want[:4], "bf16")
+        elif any(b < a for a, b in zip(off, off[1:])):
+            assert torch.all(args["out"][:max(off[-1], 0)] == 0)
+
+
+@pytest.mark.parametrize("bits,H,hkv", [(8, 4, 4), (4, 8, 2), (8, 16, 1), (4, 40, 2)])
+def test_decode_quantised(bits, H, hkv):
+    """starkv_decode_attn over codes: lengths from none to long, query positions given or not."""
+    p = Plain(H, hkv, 128, bits)
+    lens = [0, 1, 16, 17, 700, 33, 2500]
+    c = p.cache(lens)
+    for b, n in enumerate(lens):
+        if n:
+            c.fill(b, n)
+    q = p.r(torch.randn(7, H, 128, generator=torch.Generator().manual_seed(1)))
+    ws = torch.empty(p.L.workspace_bytes(7, c.pt.shape[1] * 16), dtype=torch.uint8, device="cuda").random_(0, 255)
+    for pos in (None, [3, 5, 9, 16, 10000, 1, 2499]):
+        out = torch.empty(7, p.hidden, dtype=p.dt, device="cuda")
+        p.L.decode(c.upload(), c.n_pages, c.pt_d, i32(lens), q.to(p.dt).cuda(), out, ws,
+                   q_pos=None if pos is None else i32(pos))
+        qx = p.norm_rope(q, p.wq, torch.tensor(pos if pos else [n - 1 for n in lens]))
+        want = torch.cat([R.attention(qx[b:b + 1], c.K[b], c.V[b], torch.ones(1, n, dtype=torch.bool), 128 ** -0.5)
+                          @ p.W_o if n else torch.zeros(1, p.hidden, dtype=torch.float64) for b, n in enumerate(lens)])
+        check_tree(out.to(torch.float64).cpu(), want, "bf16")
+        assert torch.all(out[0] == 0)
+    assert p.L.sync_status() == 0
+    p.L.decode(c.pool, c.n_pages, c.pt_d, i32([-1] + lens[1:6] + [5000]), q.to(p.dt).cuda(), out, ws, q_pos=i32(pos))
+    assert p.L.sync_status() == 2
 
 
 @pytest.mark.parametrize("cfg,quantized", [(1, False), (2, True), (3, True)])
