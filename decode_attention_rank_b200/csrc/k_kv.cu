@@ -84,39 +84,33 @@ __device__ __forceinline__ void angle(double turns, double* sn, double* cs) {
 // Norm and rotation of a row held as lo[V], hi[V] (channels V c .., half + V c ..) by a group of LPR lanes, in the
 // arithmetic F: float for what is rounded to 16 bits or compared in fp32, double for keys that a quantiser rounds
 // next, so that codes and scales do not depend on the order of a sum (packed pages equal the definition's bit for bit).
-template <typename F, int V, int LPR>
-__device__ __forceinline__ void norm_rotate(float* lo, float* hi, const float* w, float eps, int half, int c,
-                                            const double2* cs, bool rope) {
-  F x[V], y[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    x[k] = (F)lo[k];
-    y[k] = (F)hi[k];
-  }
-  if (w) {
+template <typename F, int V, int LPR, typename CS>
+__device__ __forceinline__ void norm_rotate(float* lo, float* hi, const float* wl, const float* wh, float eps, int half,
+                                            CS cs, bool rope) {
+  F inv = 1;
+  if (wl) {
     F s = 0;
 #pragma unroll
-    for (int k = 0; k < V; ++k) s += x[k] * x[k] + y[k] * y[k];
+    for (int k = 0; k < V; ++k) s += (F)lo[k] * (F)lo[k] + (F)hi[k] * (F)hi[k];
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const F inv = F(1) / sqrt(s / F(2 * half) + (F)eps);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      x[k] *= inv * (F)w[c * V + k];
-      y[k] *= inv * (F)w[half + c * V + k];
-    }
+    inv = F(1) / sqrt(s / F(2 * half) + (F)eps);
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    if (rope) {
-      const double2 t = cs[c * V + k];
-      const F cc = (F)t.x, ss = (F)t.y;
-      lo[k] = (float)(x[k] * cc - y[k] * ss);
-      hi[k] = (float)(y[k] * cc + x[k] * ss);
-    } else {
-      lo[k] = (float)x[k];
-      hi[k] = (float)y[k];
+    F x = lo[k], y = hi[k];
+    if (wl) {
+      x *= inv * (F)wl[k];
+      y *= inv * (F)wh[k];
     }
+    if (rope) {
+      const auto t = cs(k);
+      const F z = x * t.x - y * t.y;
+      y = y * t.x + x * t.y;
+      x = z;
+    }
+    lo[k] = (float)x;
+    hi[k] = (float)y;
   }
 }
 
@@ -141,11 +135,15 @@ __device__ __forceinline__ void quant_store(const float* x, uint8_t* blk, int sc
   const float s32 = fits ? __fmul_rn(amax, 1.f / (float)QM) : 0.f;
   const __half s16 = __float2half_ru(s32);
   const float sf = __half2float(s16);
+  // code = rne(x / s): the product with 1 / s is within 2^-21 of the quotient's size (<= 127 and a rounding), so only a
+  // product that close to a border needs the division itself
+  const float rs = sf != 0.f ? __fdiv_rn(1.f, sf) : 0.f;
   uint32_t u[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    int q = 0;
-    if (sf != 0.f) q = min(max(__float2int_rn(__fdiv_rn(x[k], sf)), -QM), QM);
+    float y = x[k] * rs;
+    if (fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f && sf != 0.f) y = __fdiv_rn(x[k], sf);
+    const int q = sf != 0.f ? min(max(__float2int_rn(y), -QM), QM) : 0;
     u[k] = (uint32_t)(q + QM + 1);
   }
   uint8_t* dst = blk + scale_bytes + (size_t)group * GB + (size_t)slot * (32 * BITS / 8) + ch * BITS / 8;
@@ -172,139 +170,125 @@ __device__ __forceinline__ void quant_store(const float* x, uint8_t* blk, int sc
   }
 }
 
-// One row (head) per group of LPR lanes; a CTA takes TOK consecutive tokens and the heads blockIdx.y, + gridDim.y ...
-// of its row groups.  The tokens' cos / sin (64-bit) are made once per CTA and shared by all heads.
-// Bound: bytes (2 loads of 16 B and their stores a lane).
-template <typename T, int D, int BITS, int TOK>
-__global__ void __launch_bounds__(kKvThreads) k_qkv(KvArgs a) {
-  constexpr int V = Vec<T>::N, HALF = D / 2, LPR = HALF / V, GROUPS = kKvThreads / LPR;
-  __shared__ double2 cs[TOK][HALF];
+// Channels c V .. of a row's two halves: norm weights of the lane, fp32.
+template <int V>
+__device__ __forceinline__ void load_w(const float* w, int half, int c, float* wl, float* wh) {
+#pragma unroll
+  for (int k = 0; k < V; k += 4) {
+    const float4 a = *reinterpret_cast<const float4*>(w + c * V + k), b = *reinterpret_cast<const float4*>(w + half + c * V + k);
+    wl[k] = a.x; wl[k + 1] = a.y; wl[k + 2] = a.z; wl[k + 3] = a.w;
+    wh[k] = b.x; wh[k + 1] = b.y; wh[k + 2] = b.z; wh[k + 3] = b.w;
+  }
+}
+
+// A CTA takes a token and up to 8 * per of its row groups (32 / LPR heads each, LPR lanes to a row; first the queries'
+// groups, then the keys', then the values'); a warp takes every 8th of them, its next group's rows loaded before this
+// one's are worked on.  The token's cos / sin are made once per CTA; a lane's pairs are the same in every head, so
+// it keeps them, like its norm weights, in registers.  Bound: bytes.  Angles: the fraction of the turn in 64 bits, then
+// an fp32 sincos; in 64 bits throughout for keys that are quantised next (see norm_rotate).
+template <typename T, int D, int BITS>
+__global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int per) {
+  constexpr int V = Vec<T>::N, HALF = D / 2, LPR = HALF / V, RPW = 32 / LPR;
+  __shared__ double2 cs_d[BITS ? HALF : 1];
+  __shared__ __align__(16) float cs_c[HALF], cs_s[HALF];
   const LayerView& v = a.v;
-  const int i0 = blockIdx.x * TOK;
-  if (a.rotate) {
-    for (int e = threadIdx.x; e < TOK * HALF; e += kKvThreads) {
-      const int i = i0 + e / HALF, p = e % HALF;
-      if (i < a.n) {
-        double sn, c;
-        angle((double)a.positions[i] * a.turn[p], &sn, &c);
-        cs[e / HALF][p] = make_double2(c, sn);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = blockIdx.x, nw = blockDim.x >> 5, b0 = blockIdx.y * nw * per, b1 = min(groups, b0 + nw * per);
+  const int g0 = b0 + warp;   // groups g0, g0 + nw, ...: the keys' and values' groups fall to different warps
+  const int nq = a.q ? (v.H + RPW - 1) / RPW : 0, nk = a.k ? (v.Hkv + RPW - 1) / RPW : 0;
+  const int c = lane % LPR, rr = lane / LPR;
+  auto source = [&](int g, bool& live) -> const T* {
+    const int kind = g < nq ? 0 : g < nq + nk ? 1 : 2;
+    const int h = (g - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * RPW + rr;
+    live = h < (kind == 0 ? v.H : v.Hkv);
+    const T* s = kind == 0 ? (const T*)a.q + (size_t)i * a.q_ld
+                           : kind == 1 ? (const T*)a.k + (size_t)i * a.k_ld : (const T*)a.vv + (size_t)i * a.v_ld;
+    return s + (size_t)h * D + c * V;
+  };
+  uint4 rl[V * sizeof(T) / 16], rh[V * sizeof(T) / 16];
+  auto fetch = [&](int g) {
+    bool live;
+    const T* s = source(g, live);
+    rl[0] = live ? *reinterpret_cast<const uint4*>(s) : make_uint4(0, 0, 0, 0);
+    rh[0] = live ? *reinterpret_cast<const uint4*>(s + HALF) : make_uint4(0, 0, 0, 0);
+  };
+  int slot = 0;
+  uint8_t* page = a.pool ? slot_page(a, i, &slot, lane == 0 && g0 == 0) : nullptr;
+  float wl[V], wh[V], cl[V], sl[V];
+  const float* w_now = nullptr;
+  if (g0 < b1) fetch(g0);
+  if (a.rotate && b0 < nq + nk) {
+    const double pos = (double)a.positions[i];
+    for (int e = threadIdx.x; e < 2 * HALF; e += blockDim.x) {
+      const int p = e % HALF;
+      if (e < HALF) {
+        const double t = pos * a.turn[p];
+        sincospif((float)(2.0 * (t - rint(t))), &cs_s[p], &cs_c[p]);
+      } else if (BITS && b1 > nq) {
+        double sn, cs;
+        angle(pos * a.turn[p], &sn, &cs);
+        cs_d[p] = make_double2(cs, sn);
       }
     }
     __syncthreads();
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(cs_c + c * V + k), y = *reinterpret_cast<const float4*>(cs_s + c * V + k);
+      cl[k] = x.x; cl[k + 1] = x.y; cl[k + 2] = x.z; cl[k + 3] = x.w;
+      sl[k] = y.x; sl[k + 1] = y.y; sl[k + 2] = y.z; sl[k + 3] = y.w;
+    }
   }
-  const int c = threadIdx.x % LPR, row0 = blockIdx.y * GROUPS + threadIdx.x / LPR;
-  const int nq = a.q ? v.H : 0, nk = a.k ? v.Hkv : 0, nv = a.vv ? v.Hkv : 0, rows = nq + nk + nv;
-  // every lane of a warp makes the same number of trips (the shuffles inside are warp-wide)
-  for (int r0 = row0; r0 - threadIdx.x / LPR < rows * TOK; r0 += gridDim.y * GROUPS) {
-    const int tok = r0 / rows, hr = r0 % rows, i = i0 + tok;
-    const bool live = r0 < rows * TOK && i < a.n;
-    const int kind = hr < nq ? 0 : (hr < nq + nk ? 1 : 2);
-    const int h = hr - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk);
-    const T* src = kind == 0 ? (const T*)a.q + (size_t)i * a.q_ld
-                             : kind == 1 ? (const T*)a.k + (size_t)i * a.k_ld : (const T*)a.vv + (size_t)i * a.v_ld;
+  for (int g = g0; g < b1; g += nw) {
+    const int kind = g < nq ? 0 : g < nq + nk ? 1 : 2;
+    const int h = (g - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * RPW + rr;
+    const bool live = h < (kind == 0 ? v.H : v.Hkv);
     float lo[V], hi[V];
-    if (live) {
-      Vec<T>::load(src + (size_t)h * D + c * V, lo);
-      Vec<T>::load(src + (size_t)h * D + HALF + c * V, hi);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) lo[k] = hi[k] = 0.f;
+    Vec<T>::load(reinterpret_cast<const T*>(rl), lo);
+    Vec<T>::load(reinterpret_cast<const T*>(rh), hi);
+    if (g + nw < b1) fetch(g + nw);
+    if (kind != 2) {
+      const float* w = kind == 0 ? v.q_norm : v.k_norm;
+      if (w && w != w_now) load_w<V>(w, HALF, c, wl, wh);
+      w_now = w;
+      if (BITS && kind == 1)
+        norm_rotate<double, V, LPR>(lo, hi, w ? wl : nullptr, wh, v.norm_eps, HALF,
+                                    [&](int k) { return cs_d[c * V + k]; }, a.rotate);
+      else
+        norm_rotate<float, V, LPR>(lo, hi, w ? wl : nullptr, wh, v.norm_eps, HALF,
+                                   [&](int k) { return make_float2(cl[k], sl[k]); }, a.rotate);
     }
-    if (BITS != 0) {
-      // keys that are quantised next go through 64-bit arithmetic; the warp takes both branches only where its rows
-      // hold keys and others
-      const bool wide = kind == 1 && a.pool != nullptr;
-      const unsigned any = __ballot_sync(0xffffffffu, wide), all = 0xffffffffu;
-      if (any) {
-        float l2[V], h2[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          l2[k] = lo[k];
-          h2[k] = hi[k];
-        }
-        norm_rotate<double, V, LPR>(l2, h2, v.k_norm, v.norm_eps, HALF, c, cs[live ? tok : 0],
-                                    a.rotate);
-        if (wide) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            lo[k] = l2[k];
-            hi[k] = h2[k];
-          }
-        }
-      }
-      if (any != all) {
-        float l2[V], h2[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          l2[k] = lo[k];
-          h2[k] = hi[k];
-        }
-        norm_rotate<float, V, LPR>(l2, h2, kind == 0 ? v.q_norm : v.k_norm, v.norm_eps, HALF, c,
-                                   cs[live ? tok : 0], a.rotate);
-        if (kind == 0 || (kind == 1 && !wide)) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            lo[k] = l2[k];
-            hi[k] = h2[k];
-          }
-        }
-      }
-    } else {
-      float l2[V], h2[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        l2[k] = lo[k];
-        h2[k] = hi[k];
-      }
-      norm_rotate<float, V, LPR>(l2, h2, kind == 0 ? v.q_norm : v.k_norm, v.norm_eps, HALF, c,
-                                 cs[live ? tok : 0], a.rotate);
-      if (kind != 2) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          lo[k] = l2[k];
-          hi[k] = h2[k];
-        }
-      }
-    }
-    if (kind == 0) {
+    if (kind == 0 || a.pool == nullptr) {
       if (live) {
-        T* o = (T*)a.q_out + (size_t)i * a.q_out_ld + (size_t)h * D;
+        T* o = (kind == 0 ? (T*)a.q_out + (size_t)i * a.q_out_ld : (T*)a.k_out + (size_t)i * a.k_out_ld) + (size_t)h * D;
         Vec<T>::store(o + c * V, lo);
         Vec<T>::store(o + HALF + c * V, hi);
       }
-    } else if (a.pool == nullptr) {
-      if (live) {
-        T* o = (T*)a.k_out + (size_t)i * a.k_out_ld + (size_t)h * D;
-        Vec<T>::store(o + c * V, lo);
-        Vec<T>::store(o + HALF + c * V, hi);
-      }
+      continue;
     }
-    if (a.pool != nullptr) {
-      int slot = 0;
-      uint8_t* page = live && kind ? slot_page(a, i, &slot, c == 0 && h == 0) : nullptr;
-      const LatentDesc& ld = v.lat[kind == 2 ? v.L - 1 : h];
-      if constexpr (BITS != 0) {
-        uint8_t* blk = page ? page + ld.block_off : nullptr;
-        const int g0 = (kind == 2 ? h * (D / 32) : 0), ch = c * V;
-        quant_store<BITS, V>(lo, blk, ld.scale_bytes, g0 + ch / 32, ch % 32, slot, page != nullptr, v.status);
-        quant_store<BITS, V>(hi, blk, ld.scale_bytes, g0 + (HALF + ch) / 32, (HALF + ch) % 32, slot, page != nullptr,
-                             v.status);
-      } else if (page) {
-        const size_t o = (size_t)slot * ld.width + (kind == 2 ? (size_t)h * D : 0) + c * V;
-        if (v.es == 4) {
-          float* d = reinterpret_cast<float*>(page + ld.block_off) + o;
+    // block of KV head h's keys, or of all values, as the page lays them out
+    if constexpr (BITS != 0) {
+      constexpr int KB = D / 32 * (32 + 64 * BITS);
+      uint8_t* blk = page ? page + (size_t)(kind == 2 ? v.Hkv : h) * KB : nullptr;
+      const int sb = kind == 2 ? v.Hkv * D : D;   // bytes of the block's scales: one per 32 channels and slot, 2 bytes
+      const int gr = kind == 2 ? h * (D / 32) : 0, ch = c * V;
+      quant_store<BITS, V>(lo, blk, sb, gr + ch / 32, ch % 32, slot, live && page, v.status);
+      quant_store<BITS, V>(hi, blk, sb, gr + (HALF + ch) / 32, (HALF + ch) % 32, slot, live && page, v.status);
+    } else if (live && page) {
+      const size_t row = kind == 2 ? ((size_t)v.Hkv * kPage + (size_t)slot * v.Hkv + h) * D
+                                   : ((size_t)h * kPage + slot) * D;
+      if (v.es == 4) {
+        float* d = reinterpret_cast<float*>(page) + row + c * V;
 #pragma unroll
-          for (int k = 0; k < V; k += 4) {
-            Vec<float>::store(d + k, lo + k);
-            Vec<float>::store(d + HALF + k, hi + k);
-          }
-        } else {
-          __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(page + ld.block_off) + o;
+        for (int k = 0; k < V; k += 4) {
+          Vec<float>::store(d + k, lo + k);
+          Vec<float>::store(d + HALF + k, hi + k);
+        }
+      } else {
+        __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(page) + row + c * V;
 #pragma unroll
-          for (int k = 0; k < V; k += 2) {
-            *reinterpret_cast<__nv_bfloat162*>(d + k) = __floats2bfloat162_rn(lo[k], lo[k + 1]);
-            *reinterpret_cast<__nv_bfloat162*>(d + HALF + k) = __floats2bfloat162_rn(hi[k], hi[k + 1]);
-          }
+        for (int k = 0; k < V; k += 2) {
+          *reinterpret_cast<__nv_bfloat162*>(d + k) = __floats2bfloat162_rn(lo[k], lo[k + 1]);
+          *reinterpret_cast<__nv_bfloat162*>(d + HALF + k) = __floats2bfloat162_rn(hi[k], hi[k + 1]);
         }
       }
     }
@@ -375,16 +359,14 @@ __global__ void __launch_bounds__(kKvThreads) k_qkv_any(KvArgs a) {
 
 template <typename T, int D, int BITS>
 cudaError_t launch_qkv_d(const KvArgs& a, cudaStream_t s) {
-  constexpr int GROUPS = kKvThreads / (D / 2 / Vec<T>::N);
-  const int rows = (a.q ? a.v.H : 0) + (a.k ? a.v.Hkv : 0) + (a.vv ? a.v.Hkv : 0);
-  // Few tokens: a token per CTA and its heads over several CTAs, for latency; many: four tokens share a CTA, whose
-  // rows then hide each other's loads.
-  if (a.n < 4 * num_sms()) {
-    const dim3 grid((unsigned)a.n, (unsigned)((rows + GROUPS - 1) / GROUPS));
-    k_qkv<T, D, BITS, 1><<<grid, kKvThreads, 0, s>>>(a);
-  } else {
-    k_qkv<T, D, BITS, 4><<<(unsigned)((a.n + 3) / 4), kKvThreads, 0, s>>>(a);
-  }
+  constexpr int RPW = 32 / (D / 2 / Vec<T>::N), NW = kKvThreads / 32;
+  const int gq = (a.v.H + RPW - 1) / RPW, gk = (a.v.Hkv + RPW - 1) / RPW;
+  const int groups = (a.q ? gq : 0) + (a.k ? gk : 0) + (a.vv ? gk : 0);
+  // Many tokens: one CTA for a whole token.  Few: a row group per warp, the token over several CTAs, for latency.
+  const bool many = (long long)a.n * groups > 64LL * num_sms();
+  const int per = many ? (groups + NW - 1) / NW : 1;
+  const int nw = std::min(NW, (groups + per - 1) / per);
+  k_qkv<T, D, BITS><<<dim3((unsigned)a.n, (unsigned)((groups + nw * per - 1) / (nw * per))), 32 * nw, 0, s>>>(a, groups, per);
   return cudaGetLastError();
 }
 
@@ -407,53 +389,82 @@ cudaError_t launch_qkv_t(const KvArgs& a, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------ reading back
-// Rows [n][latent_total] of cached tokens in TO.  One thread per 8 channels of a token where the page's bytes allow it
-// (uncompressed layers: 8 codes are 8 or 4 bytes, 8 values 16 or 32), so consecutive threads write one row in order;
-// other layers an element at a time.
-template <typename TO, int BITS>   // BITS 0: stored in the layer dtype TO
-__global__ void __launch_bounds__(256) k_read8(KvArgs a, TO* __restrict__ out) {
+// Rows [n][latent_total] of cached tokens in TO, uncompressed layers: a warp per (token, part of the row), a lane 8
+// channels at a time (8 codes are 8 or 4 bytes, 8 values 16 or 32), so that the warp's stores are one run.  The 16 warps
+// of a CTA take consecutive tokens of the same part: tokens of one page then share the 32-byte sectors of its
+// codes and scales in L1 (a slot's codes are runs of 16 or 32 bytes, its scales 2).  CPH = chunks of a head (d / 8; 0: any).
+constexpr int kReadWarps = 16;
+constexpr int kReadUnroll = 4;
+
+template <typename TO, int BITS, int CPH>   // BITS 0: stored in the layer dtype TO
+__global__ void __launch_bounds__(32 * kReadWarps) k_read8(KvArgs a, int chunks_per_warp, TO* __restrict__ out) {
   const LayerView& v = a.v;
-  const int chunks = v.Ltot / 8;
-  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (e >= (long long)a.n * chunks) return;
-  const int i = (int)(e / chunks), ch = (int)(e % chunks) * 8;
+  const int lane = threadIdx.x & 31;
+  const long long i = (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
+  if (i >= a.n) return;
+  const int cph = CPH ? CPH : v.d / 8, d = CPH ? CPH * 8 : v.d;
+  const int chunks = 2 * v.Hkv * cph;
+  const int e0 = blockIdx.y * chunks_per_warp, e1 = min(chunks, e0 + chunks_per_warp);
   int slot = 0;
-  const uint8_t* page = slot_page(a, i, &slot, ch == 0);
-  float f[8];
-  if (!page) {
+  const uint8_t* page = slot_page(a, (int)i, &slot, lane == 0 && e0 == 0);
+  TO* row = out + (size_t)i * (chunks * 8);
+  // kReadUnroll chunks' bytes are asked for before the first is used
+  for (int eb = e0 + lane; eb < e1; eb += 32 * kReadUnroll) {
+    uint4 raw[kReadUnroll][BITS == 0 && sizeof(TO) == 4 ? 2 : 1];
+    __half sc[kReadUnroll];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = 0.f;
-  } else {
-    const bool val = ch >= v.Rk;
-    const LatentDesc& ld = v.lat[val ? v.L - 1 : ch / v.d];
-    const int j = val ? ch - v.Rk : ch % v.d;
-    const uint8_t* blk = page + ld.block_off;
-    if constexpr (BITS == 0) {
-      const TO* p = reinterpret_cast<const TO*>(blk) + (size_t)slot * ld.width + j;
-#pragma unroll
-      for (int k = 0; k < 8; k += Vec<TO>::N) Vec<TO>::load(p + k, f + k);
-    } else {
-      constexpr int GB = kPage * 32 * BITS / 8;
-      const int g = j / 32;
-      const float s = __half2float(reinterpret_cast<const __half*>(blk)[g * kPage + slot]);
-      const uint8_t* c = blk + ld.scale_bytes + (size_t)g * GB + (size_t)slot * (32 * BITS / 8) + (j % 32) * BITS / 8;
-      uint32_t w[2];
-      if constexpr (BITS == 8) {
-        const uint2 u = *reinterpret_cast<const uint2*>(c);
-        w[0] = u.x;
-        w[1] = u.y;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = (float)((int)((w[k / 4] >> (8 * (k % 4))) & 255u) - 128) * s;
+    for (int x = 0; x < kReadUnroll; ++x) {
+      const int e = eb + 32 * x;
+      raw[x][0] = make_uint4(0, 0, 0, 0);
+      if constexpr (BITS == 0 && sizeof(TO) == 4) raw[x][1] = raw[x][0];
+      sc[x] = __float2half_rn(0.f);
+      if (e >= e1 || !page) continue;
+      const int h = e / cph, j = (e % cph) * 8;   // heads Hkv .. 2 Hkv - 1: values
+      const bool val = h >= v.Hkv;
+      if constexpr (BITS == 0) {
+        const size_t o = val ? ((size_t)v.Hkv * kPage + (size_t)slot * v.Hkv + (h - v.Hkv)) * d + j
+                             : ((size_t)h * kPage + slot) * d + j;
+        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const TO*>(page) + o);
+        raw[x][0] = p[0];
+        if constexpr (sizeof(TO) == 4) raw[x][1] = p[1];
       } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(c);
+        constexpr int GB = kPage * 32 * BITS / 8;
+        const int kb = d / 32 * (32 + GB);
+        const int g = (val ? (h - v.Hkv) * (d / 32) : 0) + j / 32;
+        const uint8_t* blk = page + (size_t)(val ? v.Hkv : h) * kb;
+        sc[x] = reinterpret_cast<const __half*>(blk)[g * kPage + slot];
+        const uint8_t* c = blk + (val ? v.Hkv * d : d) + (size_t)g * GB + (size_t)slot * (4 * BITS) + (j % 32) * BITS / 8;
+        if constexpr (BITS == 8) {
+          const uint2 u = *reinterpret_cast<const uint2*>(c);
+          raw[x][0].x = u.x;
+          raw[x][0].y = u.y;
+        } else {
+          raw[x][0].x = *reinterpret_cast<const uint32_t*>(c);
+        }
+      }
+    }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = (float)((int)((w[0] >> (4 * k)) & 15u) - 8) * s;
+    for (int x = 0; x < kReadUnroll; ++x) {
+      const int e = eb + 32 * x;
+      if (e >= e1) break;
+      TO* o = row + e * 8;
+      if constexpr (BITS == 0) {
+        reinterpret_cast<uint4*>(o)[0] = raw[x][0];
+        if constexpr (sizeof(TO) == 4) reinterpret_cast<uint4*>(o)[1] = raw[x][1];
+      } else {
+        float f[8];
+        const float s = __half2float(sc[x]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int u = BITS == 8 ? (int)(((k < 4 ? raw[x][0].x : raw[x][0].y) >> (8 * (k % 4))) & 255u) - 128
+                                  : (int)((raw[x][0].x >> (4 * k)) & 15u) - 8;
+          f[k] = (float)u * s;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k += Vec<TO>::N) Vec<TO>::store(o + k, f + k);
       }
     }
   }
-  TO* o = out + (size_t)i * v.Ltot + ch;
-#pragma unroll
-  for (int k = 0; k < 8; k += Vec<TO>::N) Vec<TO>::store(o + k, f + k);
 }
 
 template <typename TO>
@@ -485,7 +496,119 @@ struct AcceptArgs {
   int n_grp;
 };
 
-// One warp per (sequence, group).
+// A sequence's path, checked (flagged when it is not increasing node numbers of the sequence; the sequence is then left
+// as it was).  By the whole block; every thread gets the answer.
+__device__ __forceinline__ bool path_ok(const AcceptArgs& a, const TreeSeq& q, int n_acc, bool flag) {
+  bool ok = n_acc >= 0 && n_acc <= q.cnt;
+  for (int k = threadIdx.x; ok && k < n_acc; k += blockDim.x) {
+    const int x = a.acc[q.off + k], prev = k ? a.acc[q.off + k - 1] : -1;
+    if (x <= prev || x >= q.cnt) ok = false;
+  }
+  ok = __syncthreads_and(ok);
+  if (!ok && flag && threadIdx.x == 0) atomicOr(a.v.status, kBadPos);
+  return ok;
+}
+
+// Uncompressed layers: every group of a slot is one run of 16-byte pieces (kv_bits: 32 channels and their scale; else a
+// head's keys, and all heads' values).  A CTA takes one sequence and kAccPieces pieces of every slot, kAccNodes nodes at
+// a time: all of them into registers, then all of them out, so nothing waits for a neighbour's node.  (A later batch
+// reads slots acc[k] >= k, which earlier batches have not written.)
+constexpr int kAccNodes = 32;
+constexpr int kAccPieces = 32;      // 16-byte pieces of a slot per CTA
+constexpr int kAccThreads = 256;
+
+template <int BITS>
+__global__ void __launch_bounds__(kAccThreads) k_accept_plain(AcceptArgs a, int pieces) {
+  constexpr int PER = BITS ? BITS / 4 : 1;                                     // pieces of one group (kv_bits)
+  constexpr int IT = kAccNodes * kAccPieces / kAccThreads;
+  __shared__ long long src[kAccNodes], dst[kAccNodes];   // byte offset of the page (-1: nothing to move), per node
+  __shared__ int ss[kAccNodes], ds[kAccNodes];           // slots; ss -1: cleared
+  const LayerView& v = a.v;
+  const int b = blockIdx.y;
+  const bool first = blockIdx.x == 0;
+  const TreeSeq q = tree_seq(a.hist, a.node_off, b, a.n_nodes, a.max_nodes, a.max_pages * kPage, v.status,
+                             first && threadIdx.x == 0);
+  if (q.cnt <= 0) return;
+  const int n_acc = a.n_acc[b];
+  if (!path_ok(a, q, n_acc, first)) return;
+  for (int k0 = 0; k0 < q.cnt; k0 += kAccNodes) {
+    if (threadIdx.x < kAccNodes) {
+      const int k = k0 + threadIdx.x;
+      long long so = -1, dn = -1;
+      int s = -1, t = 0;
+      if (k < q.cnt) {
+        const bool kept = k < n_acc;
+        const int from = q.hist + (kept ? a.acc[q.off + k] : k), to = q.hist + k;
+        if (!kept || from != to) {
+          const int32_t* pt = a.pt + (size_t)b * a.max_pages;
+          const int sp = pt[from / kPage], dp = pt[to / kPage];
+          if (sp < 0 || sp >= a.n_pages || dp < 0 || dp >= a.n_pages) {
+            if (first) atomicOr(v.status, kBadPage);
+          } else {
+            so = sp * v.page_bytes;
+            dn = dp * v.page_bytes;
+            s = kept ? from % kPage : -1;
+            t = to % kPage;
+          }
+        }
+      }
+      src[threadIdx.x] = so;
+      dst[threadIdx.x] = dn;
+      ss[threadIdx.x] = s;
+      ds[threadIdx.x] = t;
+    }
+    __syncthreads();
+    uint4 x[IT];
+    __half sc[IT];
+    // piece of (block offset of slot 0, bytes from slot to slot, scale of slot 0)
+    auto where = [&](int pc, long long* at, int* step, long long* scale) {
+      if constexpr (BITS != 0) {
+        constexpr int GB = kPage * 4 * BITS;
+        const int g = pc / PER, gd = v.d / 32, kb = gd * (32 + GB);   // group of the token: keys by head, then values
+        const bool val = g >= v.Hkv * gd;
+        const int gl = val ? g - v.Hkv * gd : g % gd;
+        const long long blk = (long long)(val ? v.Hkv : g / gd) * kb;
+        *scale = pc % PER == 0 ? blk + gl * 32 : -1;
+        *at = blk + (val ? v.Hkv * v.d : v.d) + (long long)gl * GB + (pc % PER) * 16;
+        *step = 4 * BITS;
+      } else {
+        const int row = v.d * v.es, c = pc * 16, keys = v.Hkv * row;   // bytes of one head's row
+        const bool val = c >= keys;
+        *scale = -1;
+        *at = val ? (long long)kPage * keys + (c - keys) : (long long)(c / row) * kPage * row + c % row;
+        *step = val ? keys : row;
+      }
+    };
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int e = it * kAccThreads + threadIdx.x;
+      const int pl = e % PER, k = (e / PER) % kAccNodes, pc = blockIdx.x * kAccPieces + e / (PER * kAccNodes) * PER + pl;
+      x[it] = make_uint4(0, 0, 0, 0);
+      sc[it] = __float2half_rn(0.f);
+      if (pc >= pieces || src[k] < 0 || ss[k] < 0) continue;
+      long long at, scale;
+      int step;
+      where(pc, &at, &step, &scale);
+      x[it] = *reinterpret_cast<const uint4*>(a.pool + src[k] + at + (long long)ss[k] * step);
+      if (scale >= 0) sc[it] = reinterpret_cast<const __half*>(a.pool + src[k] + scale)[ss[k]];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int e = it * kAccThreads + threadIdx.x;
+      const int pl = e % PER, k = (e / PER) % kAccNodes, pc = blockIdx.x * kAccPieces + e / (PER * kAccNodes) * PER + pl;
+      if (pc >= pieces || dst[k] < 0) continue;
+      long long at, scale;
+      int step;
+      where(pc, &at, &step, &scale);
+      *reinterpret_cast<uint4*>(a.pool + dst[k] + at + (long long)ds[k] * step) = x[it];
+      if (scale >= 0) reinterpret_cast<__half*>(a.pool + dst[k] + scale)[ds[k]] = sc[it];
+    }
+    __syncthreads();
+  }
+}
+
+// Any layer: one warp per (sequence, group).
 __global__ void __launch_bounds__(256) k_accept(AcceptArgs a) {
   const LayerView& v = a.v;
   const int lane = threadIdx.x & 31;
@@ -582,22 +705,40 @@ cudaError_t launch_qkv(const KvArgs& a, bool f32, cudaStream_t s) {
   return f32 ? launch_qkv_t<float>(a, s) : launch_qkv_t<__nv_bfloat16>(a, s);
 }
 
+namespace {
+
+template <typename TO, int BITS>
+void read_plain(const KvArgs& a, void* out, cudaStream_t s) {
+  const int chunks = 2 * a.v.Hkv * (a.v.d / 8);
+  // few tokens: a row is spread over several warps, down to one round of a warp's unrolled loads
+  const long long rows = ((long long)a.n + kReadWarps - 1) / kReadWarps;
+  const int least = 32 * kReadUnroll;
+  const int parts = (int)std::max(1LL, std::min((long long)(chunks + least - 1) / least, 8LL * num_sms() / rows));
+  const int per = ((chunks + parts - 1) / parts + 31) / 32 * 32;
+  const dim3 grid((unsigned)rows, (unsigned)((chunks + per - 1) / per));
+  if (a.v.d == 128)
+    k_read8<TO, BITS, 16><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
+  else if (BITS == 0)
+    k_read8<TO, 0, 0><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
+  else if (a.v.d == 64)
+    k_read8<TO, BITS, 8><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
+  else
+    k_read8<TO, BITS, 32><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
+}
+
+}  // namespace
+
 cudaError_t launch_cache_read(const KvArgs& a, void* out, cudaStream_t s) {
   const LayerView& v = a.v;
   const bool f32 = v.dtype == STARKV_F32;
-  const long long threads = (long long)a.n * (v.Ltot / 8);
-  const unsigned grid = (unsigned)((threads + 255) / 256);
-  // eight channels a thread: rows of whole 8-channel chunks whose codes are 8 or 4 bits wide, or stored values
-  if (v.plain && v.d % 8 == 0 && (v.kv_bits || !v.quantized)) {
-    if (f32) {
-      if (v.kv_bits == 8) k_read8<float, 8><<<grid, 256, 0, s>>>(a, (float*)out);
-      else if (v.kv_bits == 4) k_read8<float, 4><<<grid, 256, 0, s>>>(a, (float*)out);
-      else k_read8<float, 0><<<grid, 256, 0, s>>>(a, (float*)out);
-    } else {
-      if (v.kv_bits == 8) k_read8<__nv_bfloat16, 8><<<grid, 256, 0, s>>>(a, (__nv_bfloat16*)out);
-      else if (v.kv_bits == 4) k_read8<__nv_bfloat16, 4><<<grid, 256, 0, s>>>(a, (__nv_bfloat16*)out);
-      else k_read8<__nv_bfloat16, 0><<<grid, 256, 0, s>>>(a, (__nv_bfloat16*)out);
-    }
+  // eight channels a lane: rows of whole 8-channel chunks
+  if (v.plain && v.d % 8 == 0) {
+    if (f32)
+      v.kv_bits == 8 ? read_plain<float, 8>(a, out, s) : v.kv_bits == 4 ? read_plain<float, 4>(a, out, s)
+                                                                        : read_plain<float, 0>(a, out, s);
+    else
+      v.kv_bits == 8 ? read_plain<__nv_bfloat16, 8>(a, out, s) : v.kv_bits == 4 ? read_plain<__nv_bfloat16, 4>(a, out, s)
+                                                                                : read_plain<__nv_bfloat16, 0>(a, out, s);
   } else {
     const unsigned gw = (unsigned)(((long long)a.n * v.L * 32 + 255) / 256);
     if (f32) k_read_any<float><<<gw, 256, 0, s>>>(a, (float*)out);
@@ -611,6 +752,18 @@ cudaError_t launch_accept(const starkv_layer* L, uint8_t* pool, long long n_page
                           const int32_t* acc, const int32_t* n_acc, cudaStream_t s) {
   AcceptArgs a{L->view, pool, n_pages, pt, max_pages, batch, n_nodes, max_nodes, hist, node_off, acc, n_acc,
                L->d_grp_lat, (int)L->grp.size()};
+  const LayerView& v = L->view;
+  const int slot_bytes = v.kv_bits ? 2 * v.Hkv * v.d * v.kv_bits / 8 : 2 * v.Hkv * v.d * v.es;
+  if (v.plain && (v.d * v.es) % 16 == 0) {
+    const int pieces = slot_bytes / 16;
+    const dim3 grid((pieces + kAccPieces - 1) / kAccPieces, batch);
+    if (batch <= 65535) {
+      if (v.kv_bits == 8) k_accept_plain<8><<<grid, kAccThreads, 0, s>>>(a, pieces);
+      else if (v.kv_bits == 4) k_accept_plain<4><<<grid, kAccThreads, 0, s>>>(a, pieces);
+      else k_accept_plain<0><<<grid, kAccThreads, 0, s>>>(a, pieces);
+      return cudaGetLastError();
+    }
+  }
   const long long warps = (long long)batch * a.n_grp;
   k_accept<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(a);
   return cudaGetLastError();

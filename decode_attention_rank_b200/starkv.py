@@ -121,23 +121,45 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
-def _rows(t, n: int, width: int, name: str):
+def _rows(t, n: int, width: int, name: str, dtype, dense: bool = False):
     """Pointer and row stride of n rows of `width` elements ([n, width] or [n, heads, d]; rows may be strided)."""
     if t is None:
         return None, 0
-    inner = t.dim() == 2 or (t.dim() == 3 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]))
-    if not inner or t.shape[0] != n or t.numel() != n * width or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be [{n}, {width}] with contiguous rows, got {list(t.shape)}")
-    return t.data_ptr(), t.stride(0) if n > 1 else width
+    shape, stride = t.shape, t.stride()
+    last = shape[-1] if shape else 0
+    if len(shape) == 3 and (shape[1] == 1 or stride[1] == last):
+        last *= shape[1]
+    elif len(shape) != 2:
+        last = -1
+    if last != width or shape[0] != n or stride[-1] != 1:
+        raise ValueError(f"{name} must be [{n}, {width}] with contiguous rows, got {list(shape)}, strides {list(stride)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must have the layer's dtype ({dtype}), got {t.dtype}")
+    if dense and n > 1 and stride[0] != width:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), stride[0] if n > 1 else width
 
 
 def _ints(t, n: int, name: str):
     """Pointer of a contiguous int32 array of n elements."""
     if t is None:
         return None
-    if t.element_size() != 4 or t.is_floating_point() or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _torch().int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 array of {n} elements")
     return t.data_ptr()
+
+
+def _table(page_table, batch: int = 0):
+    """Pointer, rows and columns of an int32 page table."""
+    rows, cols = page_table.shape
+    if rows < batch:
+        raise ValueError(f"page_table must have at least {batch} rows")
+    return _ints(page_table, rows * cols, "page_table"), rows, cols
+
+
+def _torch():
+    import torch
+    return torch
 
 
 def _stream(stream) -> int:
@@ -192,6 +214,8 @@ class LayerConfig:
 
 class Layer:
     """One loaded layer (owns its folded factors on the device)."""
+
+    _dims = None
 
     def __init__(self, handle: int, cfg: LayerConfig):
         self._h = handle
@@ -260,48 +284,43 @@ class Layer:
 
     # ---- serving an uncompressed layer, and speculative decoding (see include/starkv.h)
 
-    def _same_dtype(self, **tensors) -> None:
-        want = "torch.float32" if self.cfg.dtype == "f32" else "torch.bfloat16"
-        for name, t in tensors.items():
-            if t is not None and str(t.dtype) != want:
-                raise ValueError(f"{name} must have the layer's dtype ({want}), got {t.dtype}")
+    def _shape(self):
+        """Layer dtype, channels of a token's queries and of its keys."""
+        if self._dims is None:
+            c, torch = self.cfg, _torch()
+            self._dims = (torch.float32 if c.dtype == "f32" else torch.bfloat16, c.n_heads * c.head_dim,
+                          c.n_kv_heads * c.head_dim)
+        return self._dims
 
     def qk_norm_rope(self, q, k, positions, q_out, k_out, stream=None) -> None:
         """Per-head norm and rotation of queries and keys (either pair may be None)."""
-        self._same_dtype(q=q, k=k, q_out=q_out, k_out=k_out)
+        dt, wq, wk = self._shape()
         some = q if q is not None else k
         n = int(some.shape[0]) if some is not None else 0
-        wq, wk = self.cfg.n_heads * self.cfg.head_dim, self.cfg.n_kv_heads * self.cfg.head_dim
-        (qp, ql), (kp, kl) = _rows(q, n, wq, "q"), _rows(k, n, wk, "k")
-        (qo, qol), (ko, kol) = _rows(q_out, n, wq, "q_out"), _rows(k_out, n, wk, "k_out")
+        (qp, ql), (kp, kl) = _rows(q, n, wq, "q", dt), _rows(k, n, wk, "k", dt)
+        (qo, qol), (ko, kol) = _rows(q_out, n, wq, "q_out", dt), _rows(k_out, n, wk, "k_out", dt)
         _check(_lib.starkv_qk_norm_rope(self._h, n, _ints(positions, n, "positions"), qp, ql, kp, kl, qo, qol, ko, kol,
                                         _stream(stream)), "starkv_qk_norm_rope")
 
     def append_qkv(self, pool, n_pages: int, page_table, seq_idx, slots, q, k, v, q_out=None, positions=None,
                    stream=None) -> None:
         """Norm, rotation and storing (or quantising) of new tokens' projections in one pass."""
-        self._same_dtype(q=q, k=k, v=v, q_out=q_out)
-        n = int(seq_idx.numel())
-        wq, wk = self.cfg.n_heads * self.cfg.head_dim, self.cfg.n_kv_heads * self.cfg.head_dim
-        (qp, ql), (kp, kl), (vp, vl) = _rows(q, n, wq, "q"), _rows(k, n, wk, "k"), _rows(v, n, wk, "v")
-        qo, qol = _rows(q_out, n, wq, "q_out")
-        _check(_lib.starkv_append_qkv(self._h, _ptr(pool), n_pages, _ints(page_table, page_table.numel(), "page_table"),
-                                      int(page_table.shape[0]), int(page_table.shape[1]), n,
-                                      _ints(seq_idx, n, "seq_idx"), _ints(slots, n, "slots"),
-                                      _ints(positions, n, "positions"), qp, ql, kp, kl, vp, vl, qo, qol,
-                                      _stream(stream)), "starkv_append_qkv")
+        dt, wq, wk = self._shape()
+        n = seq_idx.numel()
+        (qp, ql), (kp, kl), (vp, vl) = _rows(q, n, wq, "q", dt), _rows(k, n, wk, "k", dt), _rows(v, n, wk, "v", dt)
+        qo, qol = _rows(q_out, n, wq, "q_out", dt)
+        pt, seqs, mp = _table(page_table)
+        _check(_lib.starkv_append_qkv(self._h, _ptr(pool), n_pages, pt, seqs, mp, n, _ints(seq_idx, n, "seq_idx"),
+                                      _ints(slots, n, "slots"), _ints(positions, n, "positions"), qp, ql, kp, kl, vp,
+                                      vl, qo, qol, _stream(stream)), "starkv_append_qkv")
 
     def cache_read(self, pool, n_pages: int, page_table, seq_idx, slots, out, stream=None) -> None:
         """Cached tokens as dense rows [n, latent_total]."""
-        self._same_dtype(out=out)
-        n = int(seq_idx.numel())
-        op, ol = _rows(out, n, self.latent_total, "out")
-        if n and ol != self.latent_total:
-            raise ValueError("out must be contiguous")
-        _check(_lib.starkv_cache_read(self._h, _ptr(pool), n_pages, _ints(page_table, page_table.numel(), "page_table"),
-                                      int(page_table.shape[0]), int(page_table.shape[1]), n,
-                                      _ints(seq_idx, n, "seq_idx"), _ints(slots, n, "slots"), op, _stream(stream)),
-               "starkv_cache_read")
+        n = seq_idx.numel()
+        op, _ = _rows(out, n, self.latent_total, "out", self._shape()[0], dense=True)
+        pt, seqs, mp = _table(page_table)
+        _check(_lib.starkv_cache_read(self._h, _ptr(pool), n_pages, pt, seqs, mp, n, _ints(seq_idx, n, "seq_idx"),
+                                      _ints(slots, n, "slots"), op, _stream(stream)), "starkv_cache_read")
 
     def tree_workspace_bytes(self, batch: int, max_ctx: int, n_nodes: int, max_nodes: int) -> int:
         return _lib.starkv_tree_workspace_bytes(self._h, batch, max_ctx, n_nodes, max_nodes)
@@ -309,21 +328,17 @@ class Layer:
     def tree_attn(self, pool, n_pages: int, page_table, hist, node_off, q, out, workspace, max_nodes: int, mask=None,
                   q_pos=None, stream=None) -> None:
         """Attention of drafted nodes over the cache: mask int32 [n_nodes, words] (bits), None = a chain."""
-        self._same_dtype(q=q, out=out)
-        batch, n = int(hist.numel()), int(q.shape[0])
+        dt, wq, _ = self._shape()
+        batch, n = hist.numel(), int(q.shape[0])
         words = 0
         if mask is not None:
             if mask.dim() != 2 or mask.shape[0] != n:
                 raise ValueError(f"mask must be [{n}, words]")
             words = int(mask.shape[1])
-        qp, ql = _rows(q, n, self.cfg.n_heads * self.cfg.head_dim, "q")
-        op, ol = _rows(out, n, self.cfg.hidden, "out")
-        if n and (ql != self.cfg.n_heads * self.cfg.head_dim or ol != self.cfg.hidden):
-            raise ValueError("q and out must be contiguous")
-        if page_table.shape[0] < batch:
-            raise ValueError(f"page_table must have at least {batch} rows")
-        _check(_lib.starkv_tree_attn(self._h, _ptr(pool), n_pages, _ints(page_table, page_table.numel(), "page_table"),
-                                     int(page_table.shape[1]), batch, _ints(hist, batch, "hist"),
+        qp, _ = _rows(q, n, wq, "q", dt, dense=True)
+        op, _ = _rows(out, n, self.cfg.hidden, "out", dt, dense=True)
+        pt, _, mp = _table(page_table, batch)
+        _check(_lib.starkv_tree_attn(self._h, _ptr(pool), n_pages, pt, mp, batch, _ints(hist, batch, "hist"),
                                      _ints(node_off, batch + 1, "node_off"), n, max_nodes,
                                      _ints(mask, n * words, "mask"), words, qp, _ints(q_pos, n, "q_pos"), op,
                                      _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -332,14 +347,11 @@ class Layer:
     def tree_accept(self, pool, n_pages: int, page_table, hist, node_off, acc, n_acc, max_nodes: int,
                     stream=None) -> None:
         """Move the accepted nodes' slots to the front and clear the other nodes' slots."""
-        batch, n = int(hist.numel()), int(acc.numel())
-        if page_table.shape[0] < batch:
-            raise ValueError(f"page_table must have at least {batch} rows")
-        _check(_lib.starkv_tree_accept(self._h, _ptr(pool), n_pages,
-                                       _ints(page_table, page_table.numel(), "page_table"), int(page_table.shape[1]),
-                                       batch, _ints(hist, batch, "hist"), _ints(node_off, batch + 1, "node_off"), n,
-                                       max_nodes, _ints(acc, n, "acc"), _ints(n_acc, batch, "n_acc"), _stream(stream)),
-               "starkv_tree_accept")
+        batch, n = hist.numel(), acc.numel()
+        pt, _, mp = _table(page_table, batch)
+        _check(_lib.starkv_tree_accept(self._h, _ptr(pool), n_pages, pt, mp, batch, _ints(hist, batch, "hist"),
+                                       _ints(node_off, batch + 1, "node_off"), n, max_nodes, _ints(acc, n, "acc"),
+                                       _ints(n_acc, batch, "n_acc"), _stream(stream)), "starkv_tree_accept")
 
     def set_decode_path(self, path: int) -> None:
         """0 automatic, 1 CUDA-core kernels, 2 tensor-core scores + CUDA-core values (diagnostics)."""
