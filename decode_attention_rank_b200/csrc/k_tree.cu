@@ -34,6 +34,8 @@ namespace {
 
 constexpr int kTreeWarps = 4;          // warps per CTA
 constexpr int kMinUnits = 2;           // pages of a warp's run, at least (short calls use fewer warps)
+constexpr int kTcRows = 128;           // rows of a row block of k_tree_tc
+constexpr int kTcTok = 128;            // tokens of its tiles
 
 template <int BITS>
 struct PageFmt {
@@ -50,8 +52,8 @@ struct TreeWs {
   long long* unit_off;   // [batch + 1] units before a sequence
   long long* item_off;   // [batch + 1] row blocks before a sequence
   void* q;               // [n_nodes][H][128] fp16 in the kernels' channel order; bf16 layers: the high, then the low parts
-  float *pm, *pl;        // [partials][16]
-  float* pY;             // [partials][16][128]
+  float *pm, *pl;        // [partials][rb]
+  float* pY;             // [partials][rb][128]
   void* y;               // output tiles
   void* part;            // output product
 };
@@ -60,8 +62,16 @@ struct TreeMma {
   LayerView v;
   TreeArgs t;
   TreeWs w;
-  int workers;           // warps of the grid
+  int workers;           // warps (k_tree_mma) or CTAs (k_tree_tc) that share the units
+  int rb;                // rows of a row block: 16, or 128
+  int unit;              // tokens of a unit: a page, or a tile of 128
+  int min_units;
 };
+
+// How a call's units are dealt: worker w takes units [w U / We, (w + 1) U / We).
+__device__ __forceinline__ long long workers_used(const TreeMma& a, long long U) {
+  return min((long long)a.workers, max(1ll, U / a.min_units));
+}
 
 __device__ __forceinline__ TreeSeq seq_of(const TreeArgs& t, int b, uint32_t* status, bool flag) {
   const int cap = t.max_pages * kPage;
@@ -95,7 +105,9 @@ __device__ __forceinline__ int warp_find(const T* off, int n, long long x, int l
 // ------------------------------------------------------------------ queries and the work list
 // Blocks (row, head group): norm, rotation, softmax scale * log2(e) of one query row per warp, rounded to fp16 (to a
 // bf16 pair high + low for bf16 caches, whose products then carry 16 bits).  The last block row: prefix sums.
-template <int BITS>
+// ORDER (4-bit codes): 0 = channels in order; 1, 2 = every eight in the order 0 4 1 5 2 6 3 7 in which the nibble masks give
+// them, with 1/16 for the odd ones (1: k_tree_mma, which meets 16 u there) or without (2: k_tree_tc).
+template <int BITS, int ORDER>
 __global__ void __launch_bounds__(128) k_tree_prep(TreeMma a) {
   const LayerView& v = a.v;
   const TreeArgs& t = a.t;
@@ -117,8 +129,8 @@ __global__ void __launch_bounds__(128) k_tree_prep(TreeMma a) {
       if (b < t.batch) {
         TreeSeq q = seq_of(t, b, v.status, true);
         if (back) q.cnt = 0;
-        ni = (long long)v.Hkv * ((q.cnt * v.group_q + 15) / 16);
-        nu = q.cnt ? ni * ((q.hist + q.cnt + kPage - 1) / kPage) : 0;
+        ni = (long long)v.Hkv * ((q.cnt * v.group_q + a.rb - 1) / a.rb);
+        nu = q.cnt ? ni * ((q.hist + q.cnt + a.unit - 1) / a.unit) : 0;
       }
       long long su = nu, si = ni;
 #pragma unroll
@@ -192,10 +204,9 @@ __global__ void __launch_bounds__(128) k_tree_prep(TreeMma a) {
     for (int k = 0; k < 4; ++k) {
       float f = (k < 2 ? x[k] : y[k - 2]) * v.scale_log2;
       int c = (k < 2 ? 0 : 64) + 2 * lane + (k & 1);
-      if (BITS == 4) {
-        // eight channels in the order 0 4 1 5 2 6 3 7 that the nibble masks give; odd ones meet 16 u
+      if (ORDER != 0) {
         const int j = c & 7;
-        if (j & 1) f *= 0.0625f;
+        if (ORDER == 1 && (j & 1)) f *= 0.0625f;
         c = (c & ~7) | ((j & 3) * 2 + (j >> 2));
       }
       o[c] = __float2half_rn(f);
@@ -312,7 +323,7 @@ __global__ void __launch_bounds__(32 * kTreeWarps, PageFmt<BITS>::CTAS) k_tree_m
   const int GQ = v.group_q;
   const long long U = a.w.unit_off[t.batch];
   const int w = warp * gridDim.x + blockIdx.x;   // neighbouring runs on different SMs
-  const long long We = min((long long)a.workers, max(1ll, U / kMinUnits));
+  const long long We = workers_used(a, U);
   if (w >= We) return;
   long long u = (long long)w * U / We;
   const long long u1 = (long long)(w + 1) * U / We;
@@ -617,6 +628,563 @@ __global__ void __launch_bounds__(32 * kTreeWarps, PageFmt<BITS>::CTAS) k_tree_m
   }
 }
 
+// ------------------------------------------------------------------ many rows: tcgen05
+// With more rows than a few warp tiles the scores and the weighted sum are products of 128-row tiles on the tensor
+// cores: S = Q K^T and O += P V over tiles of 128 tokens, Q (fp16) and P as A operands in TMEM, the codes turned into
+// fp16 tiles in shared memory once for all rows of the KV head.  K and V tiles have the same layout ([token][64
+// channels] atoms, 128-byte swizzle); K is read as a K-major operand, V as an MN-major one (its contraction runs over the
+// tokens).
+//   warps 0 - 7   dequantisation: each owns one page of every tile, with its own ring of 16-byte asynchronous copies (one
+//                 copying warp with bulk copies of 128 to 2176 bytes took 2400 cycles a tile to issue them); a lane
+//                 takes a slot's group of 32 channels, a warp 8 slots x 4 groups, so that its 16-byte stores do not conflict
+//   warp 8        MMA issue: S(0), S(1), then O += P(k) V(k) and S(k + 2)
+//   warps 9 ..    softmax, 8 warps, one row per thread: four take the even tiles, four the odd ones, so that one set's
+//                 exponentials run beside the other's loads and maxima.  The row's running maximum is handed from tile to
+//                 tile through shared memory as soon as it is known; rows past the block's are skipped by the warp.  P
+//                 overwrites S in TMEM; O is rescaled when the maximum grew by more than 2^8.
+// TMEM: S in two 128-column buffers, O in 256 .. 383, Q in 384 .. 447.  Units of work: tiles, dealt to the CTAs as above.
+constexpr int kTcDeq = 8, kTcSoft = 8;
+constexpr int kTcThreads = 32 * (1 + kTcDeq + kTcSoft);
+constexpr int kTcTile = 32768, kTcAtom = 16384;
+
+template <int BITS>
+struct TcFmt {
+  static constexpr int KB = PageFmt<BITS>::KB, VS = PageFmt<BITS>::VS;
+  static constexpr int RAW = 8 * PageFmt<BITS>::STAGE;           // 34816 or 18432 bytes: the pages of a tile
+  static constexpr int RS = BITS == 8 ? 2 : 4;                   // tiles in flight
+  static constexpr size_t SMEM = 4 * (size_t)kTcTile + (size_t)RS * RAW + 1024;
+};
+
+// One CTA's run of units, a row block's tiles at a time; by a whole warp.
+struct TcWalk {
+  long long u, u1;
+  int b, g, rb, p0, p1, len, R;
+  TreeSeq sq;
+  long long part;   // index of the partial of this row block
+};
+__device__ __forceinline__ bool tc_next(const TreeMma& a, TcWalk& s, int w, int lane) {
+  if (s.u >= s.u1) return false;
+  s.b = warp_find(a.w.unit_off, a.t.batch, s.u, lane);
+  s.sq = seq_of(a.t, s.b, a.v.status, false);
+  s.R = s.sq.cnt * a.v.group_q;
+  s.len = s.sq.hist + s.sq.cnt;
+  const int nrb = (s.R + kTcRows - 1) / kTcRows, tiles = (s.len + kTcTok - 1) / kTcTok;
+  const long long rem = s.u - a.w.unit_off[s.b];
+  const int blk = (int)(rem / tiles);
+  s.p0 = (int)(rem % tiles);
+  s.g = blk / nrb;
+  s.rb = blk % nrb;
+  s.p1 = (int)min((long long)tiles, s.p0 + (s.u1 - s.u));
+  s.part = a.w.item_off[s.b] + blk + w;
+  s.u += s.p1 - s.p0;
+  return true;
+}
+
+// Visible slots among hist + j0 .. hist + j0 + 31 for node i (row `row` of the mask), as bits: the history (j < 0), and
+// the nodes that the mask names.
+__device__ __forceinline__ uint32_t vis32(const TreeArgs& t, int row, int i, int cnt, int j0) {
+  if (j0 <= -32) return 0xffffffffu;
+  auto word = [&](int w) -> uint32_t {
+    uint32_t x;
+    if (t.mask)
+      x = w < t.mask_words ? t.mask[(size_t)row * t.mask_words + w] : 0u;
+    else
+      x = i >= 32 * w + 31 ? 0xffffffffu : i < 32 * w ? 0u : (2u << (i - 32 * w)) - 1u;
+    const int n = cnt - 32 * w;   // nodes from this word on
+    return n >= 32 ? x : n <= 0 ? 0u : x & ((1u << n) - 1u);
+  };
+  if (j0 < 0) return ((1u << -j0) - 1u) | (word(0) << -j0);
+  const int w = j0 >> 5, sh = j0 & 31;
+  return sh == 0 ? word(w) : __funnelshift_r(word(w), word(w + 1), sh);
+}
+
+__device__ __forceinline__ void tmem_ld32x(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// One lane of the converged warp, always the same.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// tc::mma_f16_ts and tc::mma_commit by the lane whose `leader` is set.
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 bd;\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+// Two fp32 numbers in one register pair, and their packed sum.
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Wait for this thread's TMEM loads; the registers pass through, so no use of them moves before it.
+__device__ __forceinline__ void tmem_wait32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])::"memory");
+}
+__device__ __forceinline__ void tmem_st16x(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32x(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+// Eight codes times their scale, fp16: 8-bit ones in channel order, 4-bit ones in the order 0 4 1 5 2 6 3 7 of the masks (Q has
+// it too; the output is put in order where it leaves TMEM).
+template <int BITS>
+__device__ __forceinline__ uint4 deq8(uint2 w, uint32_t s2) {
+  auto hmul = [](uint32_t x, uint32_t y) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  };
+  uint32_t o[4];
+  if constexpr (BITS == 8) {
+    constexpr uint32_t off = 0x64806480u, ex = 0x64646464u;
+    o[0] = hmul(hsub2(__byte_perm(w.x, ex, 0x4140), off), s2);
+    o[1] = hmul(hsub2(__byte_perm(w.x, ex, 0x4342), off), s2);
+    o[2] = hmul(hsub2(__byte_perm(w.y, ex, 0x4140), off), s2);
+    o[3] = hmul(hsub2(__byte_perm(w.y, ex, 0x4342), off), s2);
+  } else {
+    const uint32_t x = w.x, x8 = w.x >> 8;
+    constexpr uint32_t lm = 0x000F000Fu, hm = 0x00F000F0u, ex = 0x64006400u, off = 0x64086408u;
+    constexpr uint32_t s16 = 0x2C002C00u, o16 = 0xD480D480u;
+    o[0] = hmul(hsub2((x & lm) | ex, off), s2);
+    o[1] = hmul(hfma2((x & hm) | ex, s16, o16), s2);
+    o[2] = hmul(hsub2((x8 & lm) | ex, off), s2);
+    o[3] = hmul(hfma2((x8 & hm) | ex, s16, o16), s2);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
+  using F = TcFmt<BITS>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], q_full,
+      o_free, fin;
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int abort_flag;
+  __shared__ float xch[2][kTcRows], xl[2][kTcRows];   // by tile parity: row maxima handed on, and sums
+  uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* K_s = smem;                      // two stages
+  uint8_t* V_s = smem + 2 * kTcTile;        // two stages
+  uint8_t* R_s = smem + 4 * kTcTile;        // raw pages
+  const LayerView& v = a.v;
+  const TreeArgs& t = a.t;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long U = a.w.unit_off[t.batch];
+  const long long We = workers_used(a, U);
+  const int w = blockIdx.x;
+  if (w >= We || U == 0) return;
+  TcWalk wk;
+  wk.u = (long long)w * U / We;
+  wk.u1 = (long long)(w + 1) * U / We;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&k_full[s], kTcDeq);
+      tc::mbar_init(&k_empty[s], 1);
+      tc::mbar_init(&v_full[s], kTcDeq);
+      tc::mbar_init(&v_empty[s], 1);
+      tc::mbar_init(&s_full[s], 1);
+      // one barrier per tile parity, whose tiles belong to one half of the softmax warps
+      tc::mbar_init(&p_full[s], kTcSoft / 2);
+      tc::mbar_init(&o_done[s], 1);
+    }
+    tc::mbar_init(&q_full, kTcSoft);
+    tc::mbar_init(&o_free, kTcSoft);
+    tc::mbar_init(&fin, 1);
+    abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == kTcDeq) tc::tmem_alloc(&tmem_base, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  constexpr uint32_t o_col = 256, q_col = 384;
+
+  if (warp == kTcDeq) {
+    // ------------------------------------------------ MMA issue
+    const uint32_t idesc_s = tc::idesc_f16(128, 128, false, false, false);
+    const uint32_t idesc_o = tc::idesc_f16(128, 128, false, false, true);   // V: tokens are the contraction
+    const uint64_t dk = tc::sdesc_sw128(tc::smem_u32(K_s), 0, 1024);
+    const uint64_t dv = tc::sdesc_sw128(tc::smem_u32(V_s), kTcAtom, 1024);  // 64 channels to the next, 8 tokens to the next
+    const uint32_t k_lo = tc::desc_lo(dk), k_hi = tc::desc_hi(dk), v_lo = tc::desc_lo(dv), v_hi = tc::desc_hi(dv);
+    // The whole warp walks the loop and one elected lane issues, by a predicate on the instruction: the control flow stays
+    // uniform, so descriptors and addresses stay in uniform registers (issued from a branch of one lane, an MMA took about 100
+    // cycles to issue, more than its execution).
+    const uint32_t leader = elect_one();
+    bool ok = true;
+    int jg = 0, n = 0;   // tiles and row blocks so far
+    auto issue_s = [&](int j) -> bool {
+      const int s = j & 1;
+      if (!tc::mbar_wait_ab(&k_full[s], ((uint32_t)(j >> 1)) & 1u, v.status, &abort_flag)) return false;
+      tc::tc_fence_after();
+      // S buffer j & 1 is free: P(j - 2) V(j - 2), issued before, has read it by the time these run (a block's first two
+      // tiles: the last block's products have completed, its softmax warps have said so by q_full)
+      const uint32_t d = tmem + (uint32_t)(s * 128), b = k_lo + (uint32_t)(s * kTcTile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(leader, d, tmem + q_col + 8u * kk, b + (uint32_t)(kk >> 2) * (kTcAtom >> 4) + 2u * (kk & 3), k_hi, idesc_s,
+               kk ? 1u : 0u);
+      commit(leader, &s_full[s]);
+      commit(leader, &k_empty[s]);
+      return true;
+    };
+    while (ok && tc_next(a, wk, w, lane)) {
+      const int nt = __shfl_sync(0xffffffffu, wk.p1 - wk.p0, 0);
+      ok = tc::mbar_wait_ab(&q_full, (uint32_t)n & 1u, v.status, &abort_flag);
+      tc::tc_fence_after();
+      ok = ok && issue_s(jg) && (nt == 1 || issue_s(jg + 1));
+      for (int k = 0; ok && k < nt; ++k) {
+        const int j = jg + k, s = j & 1;
+        if (k == 0 && !(ok = tc::mbar_wait_ab(&o_free, ((uint32_t)n & 1u) ^ 1u, v.status, &abort_flag))) break;
+        if (!(ok = tc::mbar_wait_ab(&v_full[s], ((uint32_t)(j >> 1)) & 1u, v.status, &abort_flag))) break;
+        if (!(ok = tc::mbar_wait_ab(&p_full[s], ((uint32_t)(j >> 1)) & 1u, v.status, &abort_flag))) break;
+        tc::tc_fence_after();
+        const uint32_t p = tmem + (uint32_t)(s * 128), b = v_lo + (uint32_t)(s * kTcTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(leader, tmem + o_col, p + 8u * kk, b + (uint32_t)(kk * 2048 >> 4), v_hi, idesc_o, (k | kk) ? 1u : 0u);
+        commit(leader, &o_done[s]);
+        commit(leader, &v_empty[s]);
+        if (k + 2 < nt && !(ok = issue_s(j + 2))) break;
+      }
+      jg += nt;
+      ++n;
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (!ok) abort_flag = 1;
+    commit(leader, &fin);
+    tc::mbar_wait(&fin, 0, v.status);   // every MMA has completed before the CTA may exit
+    __syncwarp();
+  } else if (warp < kTcDeq) {
+    // ------------------------------------------------ dequantisation: page `warp` of every tile
+    const int sl = lane & 7, gr = lane >> 3;   // slot of a half page, group of 32 channels
+    // this lane's stores: chunk c of its group is 16-byte chunk 4 (gr % 2) + c of atom gr / 2, at that ^ (row % 8 = slot)
+    const uint32_t st0 = (uint32_t)(gr >> 1) * kTcAtom + (uint32_t)warp * 2048u + (uint32_t)sl * 128u;
+    const uint32_t st1 = (uint32_t)((4 * (gr & 1)) ^ sl) << 4;
+    uint8_t* ring = R_s + (size_t)warp * F::RS * PageFmt<BITS>::STAGE;
+    const uint32_t ring_s = tc::smem_u32(ring);
+    bool ok = true;
+    int n = 0;
+    while (ok && tc_next(a, wk, w, lane)) {
+      const int32_t* pt = t.pt + (size_t)wk.b * t.max_pages;
+      const int pages = (wk.len + kPage - 1) / kPage;
+      int ids0 = wk.p0, next = wk.p0;
+      auto fetch_ids = [&]() {   // this warp's page of 32 tiles; -2: past the sequence's pages
+        const int p = (ids0 + lane) * 8 + warp;
+        return ids0 + lane < wk.p1 ? (p < pages ? max(pt[p], -1) : -2) : -2;
+      };
+      int ids = fetch_ids();
+      auto issue = [&]() {
+        if (next < wk.p1) {
+          if (next - ids0 == 32) {
+            ids0 = next;
+            ids = fetch_ids();
+          }
+          const int page = __shfl_sync(0xffffffffu, ids, next - ids0);
+          // past the sequence's pages the stage keeps what it held: those tokens' scales are set to zero
+          if (page != -2)
+            issue_page<BITS>(a, page, wk.g, ring_s + (uint32_t)((next - wk.p0) % F::RS) * PageFmt<BITS>::STAGE, lane);
+          ++next;
+        }
+        cp_commit();
+      };
+#pragma unroll
+      for (int k = 0; k < F::RS - 1; ++k) issue();
+      for (int k = wk.p0; k < wk.p1 && ok; ++k, ++n) {
+        const int s = n & 1;
+        cp_wait<F::RS - 2>();
+        __syncwarp();   // this page's bytes from every lane; every lane is done with the stage that is filled next
+        issue();
+        const uint8_t* raw = ring + (size_t)((k - wk.p0) % F::RS) * PageFmt<BITS>::STAGE;
+        const int tokens = wk.len - (k * kTcTok + warp * 16);   // of this page
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+          const uint8_t* sc = (side ? raw + F::KB : raw) + 32 * gr + 2 * sl;
+          const uint8_t* cd = (side ? raw + F::KB + F::VS : raw + 128) + gr * (64 * BITS) + sl * (4 * BITS);
+          // all loads first: the compiler keeps a load behind a store that may alias it
+          uint4 code[2][BITS / 4];
+          uint32_t scale[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < BITS / 4; ++i) code[half][i] = *reinterpret_cast<const uint4*>(cd + half * (32 * BITS) + i * 16);
+            scale[half] = *reinterpret_cast<const uint16_t*>(sc + half * 16);
+          }
+          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_ab(side ? &v_empty[s] : &k_empty[s], (((uint32_t)(n >> 1)) & 1u) ^ 1u, v.status, &abort_flag));
+          if (ok) {
+            uint8_t* tile = (side ? V_s : K_s) + (size_t)s * kTcTile + st0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              // slots without a token may hold any bytes: their scale is zero
+              const uint32_t h = half * 8 + sl < tokens ? scale[half] : 0u, s2 = __byte_perm(h, 0u, 0x1010);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint4& w4 = code[half][BITS == 8 ? c >> 1 : 0];
+                uint2 x;
+                if constexpr (BITS == 8)
+                  x = c & 1 ? make_uint2(w4.z, w4.w) : make_uint2(w4.x, w4.y);
+                else
+                  x = make_uint2(c == 0 ? w4.x : c == 1 ? w4.y : c == 2 ? w4.z : w4.w, 0u);
+                *reinterpret_cast<uint4*>(tile + half * 1024 + (((uint32_t)c << 4) ^ st1)) = deq8<BITS>(x, s2);
+              }
+            }
+            tc::fence_proxy_async();
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(side ? &v_full[s] : &k_full[s]);
+        }
+      }
+      cp_wait<0>();
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------ softmax and output
+    const int qq = warp & 3, x = (warp - 1 - kTcDeq) >> 2;   // TMEM lane quarter; tiles of this parity
+    const int r = qq * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(qq * 32) << 16;
+    const uint32_t s_at = tmem + lane_base + 128u * x, o_at = tmem + lane_base + o_col;
+    // named barriers of the two warps of a quarter: 1 + 2 qq + parity hands on the maximum after a tile of that
+    // parity, 9 + qq joins the sums
+    const int bar_out = 1 + 2 * qq + x, bar_in = 1 + 2 * qq + (x ^ 1), bar_l = 9 + qq;
+    bool ok = true;
+    int jg = 0;
+    while (tc_next(a, wk, w, lane)) {
+      const int row = wk.rb * kTcRows + r;                       // row of the sequence and KV head
+      const bool warp_live = wk.rb * kTcRows + qq * 32 < wk.R;   // some row of this warp is real
+      const int node = row / v.group_q;
+      // ---- this row's Q: 64 of its channels (32 columns) into TMEM.  The last block's MMAs have completed (o_done).
+      {
+        uint32_t qv[32];
+        const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)a.w.q +
+                                                          ((size_t)(wk.sq.off + node) * v.H + wk.g * v.group_q + row % v.group_q) * 128 + 64 * x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 z = row < wk.R ? src[c] : make_uint4(0, 0, 0, 0);
+          qv[4 * c] = z.x;
+          qv[4 * c + 1] = z.y;
+          qv[4 * c + 2] = z.z;
+          qv[4 * c + 3] = z.w;
+        }
+        tmem_st32x(tmem + lane_base + q_col + 32u * x, qv);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&q_full);
+      }
+      float m_used = -1e30f, l = 0.f;   // l is the sum of this parity's tiles, in units of 2^m_used
+      const int nt = wk.p1 - wk.p0;
+      for (int k = (jg & 1) == x ? 0 : 1; k < nt; k += 2) {
+        const int j = jg + k;
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_ab(&s_full[x], ((uint32_t)(j >> 1)) & 1u, v.status, &abort_flag));
+        tc::tc_fence_after();
+        if (warp_live) {   // (also after an abort: the two warps of a quarter meet at their barriers, over old columns)
+          const int t0 = (wk.p0 + k) * kTcTok;
+          const bool tail = t0 + kTcTok > wk.sq.hist;   // the tile holds drafted nodes or unused slots
+          if (tail) {   // what a row does not see becomes -infinity in TMEM
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              float s[32];
+              const uint32_t see = row < wk.R ? vis32(t, wk.sq.off + node, node, wk.sq.cnt, t0 + 32 * h - wk.sq.hist) : 0u;
+              tmem_ld32x(s_at + 32u * h, s);
+              tmem_wait32(s);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(see >> c & 1u)) s[c] = -INFINITY;
+              tmem_st32x(s_at + 32u * h, reinterpret_cast<const uint32_t*>(s));
+            }
+            tc::tmem_st_wait();
+          }
+          // S in four pieces of 32 columns, twice: for the maximum, and for the exponentials; each piece is asked for while
+          // the one before is worked on
+          float s0[32], s1[32];
+          auto top = [](const float* s) {
+            float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          };
+          tmem_ld32x(s_at, s0);
+          tmem_wait32(s0);
+          tmem_ld32x(s_at + 32u, s1);
+          float mx = top(s0);
+          tmem_wait32(s1);
+          tmem_ld32x(s_at + 64u, s0);
+          mx = fmaxf(mx, top(s1));
+          tmem_wait32(s0);
+          tmem_ld32x(s_at + 96u, s1);
+          mx = fmaxf(mx, top(s0));
+          tmem_wait32(s1);
+          tmem_ld32x(s_at, s0);
+          mx = fmaxf(mx, top(s1));
+          float m_prev = m_used;
+          if (k > 0) {   // the maximum as the other parity's tile left it
+            asm volatile("bar.sync %0, 64;" ::"r"(bar_in) : "memory");
+            m_prev = xch[x ^ 1][r];
+          }
+          const float m_new = mx > m_prev + 8.f ? mx : m_prev;
+          xch[x][r] = m_new;
+          asm volatile("bar.arrive %0, 64;" ::"r"(bar_out) : "memory");
+          l *= ex2(m_used - m_new);
+          m_used = m_new;
+          // O is in units of 2^m_prev until here
+          if (k > 0 && __any_sync(0xffffffffu, m_new != m_prev)) {
+            // (S(j) is complete, so O += P(j - 2) V(j - 2), issued before it, is too: the wait is for the phase meant)
+            ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_ab(&o_done[x ^ 1], ((uint32_t)((j - 1) >> 1)) & 1u, v.status, &abort_flag));
+            tc::tc_fence_after();
+            if (ok) {
+              const float f = ex2(m_prev - m_new);
+#pragma unroll 1
+              for (int c = 0; c < 128; c += 16) {
+                float o[16];
+                uint32_t ou[16];
+                tc::tmem_ld16_sync(o_at + (uint32_t)c, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ou[i] = __float_as_uint(o[i] * f);
+                tc::tmem_st8(o_at + (uint32_t)c, ou);
+                tc::tmem_st8(o_at + (uint32_t)c + 8, ou + 8);
+              }
+              tc::tmem_st_wait();
+            }
+          }
+          // P over columns of S that have been read: 16 columns of pairs for 32 of scores
+          unsigned long long l2[4] = {0ull, 0ull, 0ull, 0ull};   // packed pairs of sums
+          const unsigned long long nm = pack2(-m_used, -m_used);
+          auto put = [&](uint32_t at, const float* s) {
+            uint32_t p2[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 d = unpack2(add2(pack2(s[c], s[c + 1]), nm));
+              const float e0 = ex2(d.x), e1 = ex2(d.y);
+              l2[(c >> 1) & 3] = add2(l2[(c >> 1) & 3], pack2(e0, e1));
+              p2[c / 2] = h2(e0, e1);
+            }
+            tmem_st16x(at, p2);
+          };
+          tmem_wait32(s0);
+          tmem_ld32x(s_at + 32u, s1);
+          put(s_at, s0);
+          tmem_wait32(s1);
+          tmem_ld32x(s_at + 64u, s0);
+          put(s_at + 16u, s1);
+          tmem_wait32(s0);
+          tmem_ld32x(s_at + 96u, s1);
+          put(s_at + 32u, s0);
+          tmem_wait32(s1);
+          put(s_at + 48u, s1);
+          const float2 ls = unpack2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
+          l += ls.x + ls.y;
+          tc::tmem_st_wait();
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[x]);
+      }
+      jg += nt;
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_ab(&o_done[(jg - 1) & 1], ((uint32_t)((jg - 1) >> 1)) & 1u, v.status, &abort_flag));
+      tc::tc_fence_after();
+      if (warp_live) {
+        // the final maximum: the last tile's warp has it, the other takes its last hand-over
+        float m_end = m_used;
+        if (((jg - 1) & 1) != x) {
+          asm volatile("bar.sync %0, 64;" ::"r"(bar_in) : "memory");
+          m_end = xch[x ^ 1][r];
+        }
+        xl[x][r] = l * ex2(m_used - m_end);
+        asm volatile("bar.sync %0, 64;" ::"r"(bar_l) : "memory");
+        l = xl[0][r] + xl[1][r];
+        if (x == 0 && row < wk.R) {
+          a.w.pm[wk.part * kTcRows + r] = m_end;
+          a.w.pl[wk.part * kTcRows + r] = ok ? l : 0.f;
+        }
+        float* y = a.w.pY + (wk.part * kTcRows + r) * 128 + 64 * x;
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          float o[16];
+          if (ok)
+            tc::tmem_ld16_sync(o_at + 64u * x + (uint32_t)c, o);
+          else
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = 0.f;
+          if (row < wk.R) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) {
+              float4* d = reinterpret_cast<float4*>(y + c + i);
+              if constexpr (BITS == 4) {
+                d[0] = make_float4(o[i], o[i + 2], o[i + 4], o[i + 6]);
+                d[1] = make_float4(o[i + 1], o[i + 3], o[i + 5], o[i + 7]);
+              } else {
+                d[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                d[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+              }
+            }
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&o_free);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == kTcDeq) tc::tmem_dealloc(tmem, 512);
+}
+
 // ------------------------------------------------------------------ merging the partials
 // One warp per (output row, query head), lane: four channels.  Writes y as fp16 into the output product's B tiles;
 // rows of no sequence and the tiles' padding rows are zero.
@@ -637,20 +1205,20 @@ __global__ void __launch_bounds__(256) k_tree_combine(TreeMma a, int rows_pad, i
     const TreeSeq sq = seq_of(t, b, v.status, false);
     if (sq.cnt > 0 && row >= sq.off && row - sq.off < sq.cnt && a.w.item_off[b + 1] > a.w.item_off[b]) {
       const int g = h / v.group_q, rr = (row - sq.off) * v.group_q + h % v.group_q;
-      const int nrb = (sq.cnt * v.group_q + 15) / 16, pages = (sq.hist + sq.cnt + kPage - 1) / kPage;
-      const int blk = g * nrb + rr / 16, r = rr % 16;
+      const int nrb = (sq.cnt * v.group_q + a.rb - 1) / a.rb, units = (sq.hist + sq.cnt + a.unit - 1) / a.unit;
+      const int blk = g * nrb + rr / a.rb, r = rr % a.rb;
       const long long U = a.w.unit_off[t.batch];
-      const long long We = min((long long)a.workers, max(1ll, U / kMinUnits));
-      const long long lo = a.w.unit_off[b] + (long long)blk * pages, hi = lo + pages - 1;
+      const long long We = workers_used(a, U);
+      const long long lo = a.w.unit_off[b] + (long long)blk * units, hi = lo + units - 1;
       const long long w0 = ((lo + 1) * We - 1) / U, w1 = ((hi + 1) * We - 1) / U;   // the warps of the first, last unit
       const long long base = a.w.item_off[b] + blk;
       float m = -FLT_MAX, l = 0.f;
-      for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, a.w.pm[(base + w) * 16 + r]);
+      for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, a.w.pm[(base + w) * a.rb + r]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll 4
       for (long long w = w0; w <= w1; ++w) {
-        const long long p = (base + w) * 16 + r;
+        const long long p = (base + w) * a.rb + r;
         const float f = ex2(a.w.pm[p] - m);
         const float4 x = *reinterpret_cast<const float4*>(a.w.pY + p * 128 + lane * 4);
         l += f * a.w.pl[p];
@@ -679,17 +1247,25 @@ int tree_workers(int kv_bits) {
 struct TreePlan {
   size_t unit_off, item_off, q, pm, pl, pY, y, part, total;
   int NB, rows_pad;
+  bool tc;               // k_tree_tc
+  int workers, rb;
 };
+
+// Rows per sequence and KV head from which the 128-row kernel is taken.
+constexpr int kTcFrom = 33;
 
 TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
   const LayerView& v = L->view;
   TreePlan p;
   p.NB = outproj_nb(n_nodes);
   p.rows_pad = (n_nodes + p.NB - 1) / p.NB * p.NB;
-  // row blocks: 16 rows each, one more per sequence for what its last block leaves empty
-  const size_t items = (size_t)v.Hkv * std::min((size_t)batch * ((max_nodes * v.group_q + 15) / 16),
-                                                (size_t)batch + (size_t)n_nodes * v.group_q / 16);
-  const size_t parts = items + tree_workers(v.kv_bits);
+  // row blocks of 16 or 128 rows, one more per sequence for what its last block leaves empty
+  p.tc = v.kv_bits != 0 && max_nodes * v.group_q >= kTcFrom;
+  p.workers = p.tc ? num_sms() : tree_workers(v.kv_bits);
+  p.rb = p.tc ? kTcRows : 16;
+  const size_t items = (size_t)v.Hkv * std::min((size_t)batch * ((max_nodes * v.group_q + p.rb - 1) / p.rb),
+                                                (size_t)batch + (size_t)n_nodes * v.group_q / p.rb);
+  const size_t parts = items + p.workers;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -699,9 +1275,9 @@ TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes)
   p.unit_off = take(8 * ((size_t)batch + 1));
   p.item_off = take(8 * ((size_t)batch + 1));
   p.q = take((size_t)n_nodes * v.H * 256 * (v.kv_bits == 0 ? 2 : 1));
-  p.pm = take(parts * 64);
-  p.pl = take(parts * 64);
-  p.pY = take(parts * 16 * 512);
+  p.pm = take(parts * p.rb * 4);
+  p.pl = take(parts * p.rb * 4);
+  p.pY = take(parts * p.rb * 512);
   p.y = take((size_t)p.rows_pad / p.NB * (L->Kp / 64) * p.NB * 128);
   p.part = take(outproj_part_bytes(L, n_nodes));
   p.total = o;
@@ -712,15 +1288,24 @@ template <int BITS>
 cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cudaStream_t s) {
   using F = PageFmt<BITS>;
   const LayerView& v = L->view;
-  k_tree_prep<BITS><<<dim3(a.t.n_nodes + 1, (v.H + kTreeWarps - 1) / kTreeWarps), 32 * kTreeWarps, 0, s>>>(a);
+  const dim3 pgrid(a.t.n_nodes + 1, (v.H + kTreeWarps - 1) / kTreeWarps);
+  if (BITS == 4 && !p.tc)
+    k_tree_prep<BITS, 1><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
+  else if (BITS == 4)
+    k_tree_prep<BITS, 2><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
+  else
+    k_tree_prep<BITS, 0><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (BITS != 0 && p.tc) {
+    constexpr int B = BITS == 0 ? 8 : BITS;
+    if ((e = set_smem_limit((const void*)k_tree_tc<B>, TcFmt<B>::SMEM)) != cudaSuccess) return e;
+    k_tree_tc<B><<<a.workers, kTcThreads, TcFmt<B>::SMEM, s>>>(a);
+    return cudaGetLastError();
+  }
   const size_t smem = (size_t)kTreeWarps * F::NS * F::STAGE;
   if ((e = set_smem_limit((const void*)k_tree_mma<BITS>, smem)) != cudaSuccess) return e;
   k_tree_mma<BITS><<<a.workers / kTreeWarps, 32 * kTreeWarps, smem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long warps = (long long)p.rows_pad * v.H;
-  k_tree_combine<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(a, p.rows_pad, p.NB, L->Kp / 64);
   return cudaGetLastError();
 }
 
@@ -748,10 +1333,16 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
   a.w.pY = (float*)(w + p.pY);
   a.w.y = w + p.y;
   a.w.part = w + p.part;
-  a.workers = tree_workers(v.kv_bits);
+  a.workers = p.workers;
+  a.rb = p.rb;
+  a.unit = p.tc ? kTcTok : kPage;
+  a.min_units = p.tc ? 1 : kMinUnits;
   cudaError_t e = v.kv_bits == 8 ? launch_bits<8>(L, a, p, s) : v.kv_bits == 4 ? launch_bits<4>(L, a, p, s)
                                                                                : launch_bits<0>(L, a, p, s);
   if (e != cudaSuccess) return e;
+  const long long warps = (long long)p.rows_pad * v.H;
+  k_tree_combine<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(a, p.rows_pad, p.NB, L->Kp / 64);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_outproj_tc(L, a.w.y, t.n_nodes, t.out, (float*)a.w.part, s, t.lens ? nullptr : t.node_off + t.batch);
 }
 

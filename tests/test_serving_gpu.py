@@ -350,7 +350,7 @@ TREES = [
     # H, hkv, hist, counts
     (4, 4, [0], [1]), (4, 4, [1], [1]), (4, 2, [15, 0, 16], [1, 1, 1]), (8, 1, [333], [7]),
     (4, 4, [31, 700, 0, 5], [16, 3, 9, 0]), (4, 1, [130, 1025], [33, 64]), (16, 2, [40, 250], [24, 13]),
-    (2, 2, [257], [100]), (4, 2, [9, 9, 9] * 23, [1, 2, 0] * 23), (32, 8, [77, 5], [24, 31]), (8, 8, [2000, 1999], [5, 8])]
+    (2, 2, [257], [100]), (8, 1, [100, 3000, 0], [64, 40, 33]), (32, 2, [5, 640], [3, 20]), (4, 1, [1000] * 9, [9] * 9), (4, 2, [9, 9, 9] * 23, [1, 2, 0] * 23), (32, 8, [77, 5], [24, 31]), (8, 8, [2000, 1999], [5, 8])]
 
 
 @pytest.mark.parametrize("bits", [0, 8, 4])
