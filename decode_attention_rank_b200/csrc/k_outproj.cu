@@ -181,13 +181,17 @@ __global__ void __launch_bounds__(kOutThreads, 1) k_outproj_tc(OutArgs a) {
   if (warp == 1) tc::tmem_dealloc(tmem, a.tmem_cols);
 }
 
-// out[row][n] = sum over the CTAs whose k-range touched output tile n / 128.
+// out[row][n] = sum over the CTAs whose k-range touched output tile n / 128.  A block takes `per` <= kReduceRows rows: one
+// for few rows (as many blocks as there are), four for many.
+constexpr int kReduceRows = 4;
 template <typename TO>
 __global__ void k_outproj_reduce(const float* __restrict__ part, int G, int KT, int DT, int slots, int NB, int rows,
-                                 int D, const int32_t* __restrict__ n_rows, TO* __restrict__ out) {
+                                 int D, const int32_t* __restrict__ n_rows, int per, TO* __restrict__ out) {
   __shared__ long long seg_off[512];
-  const int dt = blockIdx.x, row = blockIdx.y;
-  if (n_rows && row >= *n_rows) return;
+  // kReduceRows rows of one row tile (NB is a multiple of 16): their segments lie at the same places, one row apart
+  const int dt = blockIdx.x, row = blockIdx.y * per;
+  if (n_rows) rows = min(rows, *n_rows);
+  if (row >= rows) return;
   const int nt = row / NB, b = row % NB;
   // The CTAs whose unit ranges [begin(c), begin(c + 1)) meet this output
   // tile's k-range [lo, hi): candidates c_lo, c_lo + 1, ... tested one per
@@ -211,12 +215,19 @@ __global__ void k_outproj_reduce(const float* __restrict__ part, int G, int KT, 
   for (int n = threadIdx.x; n < 128; n += blockDim.x) {
     const int d = dt * 128 + n;
     if (d >= D) continue;
-    float acc = 0.f;
+    float acc[kReduceRows];
+#pragma unroll
+    for (int i = 0; i < kReduceRows; ++i) acc[i] = 0.f;
     for (int k = 0; k < nc; ++k) {
       const long long o = seg_off[k];
-      if (o >= 0) acc += part[o + n];
+      if (o < 0) continue;
+#pragma unroll
+      for (int i = 0; i < kReduceRows; ++i)
+        if (i < per && row + i < rows) acc[i] += part[o + n + i * 128];
     }
-    out[(size_t)row * D + d] = (TO)acc;
+#pragma unroll
+    for (int i = 0; i < kReduceRows; ++i)
+      if (i < per && row + i < rows) out[(size_t)(row + i) * D + d] = (TO)acc[i];
   }
 }
 
@@ -291,12 +302,14 @@ cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, con
     at.part = part + (size_t)t * g.G * g.slots * NB * 128;
     k_outproj_tc<<<dim3(g.G, 1), kOutThreads, smem, s>>>(at);
   }
+  const int per = rows > 32 ? kReduceRows : 1;
+  const dim3 rgrid(g.DT, (rows + per - 1) / per);
   if (out_f32)
-    k_outproj_reduce<float><<<dim3(g.DT, rows), 128, 0, s>>>(part, g.G, g.KT, g.DT, g.slots, NB, rows, n_valid,
-                                                             n_rows, (float*)out);
+    k_outproj_reduce<float><<<rgrid, 128, 0, s>>>(part, g.G, g.KT, g.DT, g.slots, NB, rows, n_valid, n_rows, per,
+                                                  (float*)out);
   else
-    k_outproj_reduce<__nv_bfloat16><<<dim3(g.DT, rows), 128, 0, s>>>(part, g.G, g.KT, g.DT, g.slots, NB, rows,
-                                                                     n_valid, n_rows, (__nv_bfloat16*)out);
+    k_outproj_reduce<__nv_bfloat16><<<rgrid, 128, 0, s>>>(part, g.G, g.KT, g.DT, g.slots, NB, rows, n_valid, n_rows, per,
+                                                          (__nv_bfloat16*)out);
   return cudaGetLastError();
 }
 

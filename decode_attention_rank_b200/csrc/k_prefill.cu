@@ -301,6 +301,7 @@ struct GemmArgs {
   void* out;            // EPI_VT / EPI_KROPE: tiles [blockIdx.y][n_tiles]; EPI_OUT: row-major [rows][ld]
   int n_tiles;
   int rows, n_valid, ld;   // EPI_OUT
+  const int32_t* n_rows;   // EPI_OUT: rows in use (device; null: all)
   const uint8_t* E;        // EPI_KROPE: RoPE table (null: no rotation)
   uint32_t* status;
 };
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_full(GemmArgs a) {
         }
       }
     }
+    const int rows = (EPI == EPI_OUT_BF16 || EPI == EPI_OUT_F32) && a.n_rows ? min(a.rows, *a.n_rows) : a.rows;
     for (int c0 = 0; c0 < (EPI == EPI_KROPE ? 0 : 128); c0 += 16) {
       float x[16];
       if (ok) {
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_full(GemmArgs a) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int row = blockIdx.x * 128 + c0 + i;
-            if (row < a.rows) {
+            if (row < rows) {
               if constexpr (EPI == EPI_OUT_F32)
                 reinterpret_cast<float*>(a.out)[(size_t)row * a.ld + col] = x[i];
               else
@@ -945,15 +947,24 @@ cudaError_t launch_prefill_flash(const starkv_layer* L, const uint8_t* pool, lon
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // out = y W_o: y as fp16 B tiles of 128 rows, W_o as the A tiles
   if ((e = launch_pack_rows_tiles_f32(w.y, q_len, v.H * 128, w.yt, s, 128)) != cudaSuccess) return e;
+  return launch_out_full(L, w.yt, q_len, out, nullptr, s);
+}
+
+cudaError_t launch_out_full(const starkv_layer* L, const void* yt, int rows, void* out, const int32_t* n_rows,
+                            cudaStream_t s) {
+  const LayerView& v = L->view;
+  cudaError_t e;
+  const int n_qt = (rows + kT - 1) / kT;
   GemmArgs go{};
   go.A = (const uint8_t*)prefill_wo_tiles(L);
   go.a_step_y = (long long)(v.H * 128 / 64) * kAtomB;
-  go.B = w.yt;
+  go.B = (const uint8_t*)yt;
   go.b_step_x = (long long)(v.H * 128 / 64) * kAtomB;
   go.KT = v.H * 128 / 64;
   go.stages = std::min(3, go.KT);
   go.out = out;
-  go.rows = q_len;
+  go.rows = rows;
+  go.n_rows = n_rows;
   go.n_valid = v.D;
   go.ld = v.D;
   go.status = v.status;

@@ -1,29 +1,32 @@
 // Attention of drafted tokens (nodes of a tree, a chain, or one token) over an
 // uncompressed layer's cache: bf16 K and V, or their 8 / 4-bit codes.
 //
-// Every KV head's R = nodes * group rows of a sequence share its K and V, so a
-// page (16 tokens) is read once for up to 16 rows, the M side of the warp-level
-// matrix instruction m16n8k16.  The codes go from shared memory into MMA
-// operands without being scaled first:
-//   scores   a code byte u under the fp16 exponent of 1024 is the number 1024 + u (one PRMT per two codes; 4-bit codes
-//            in a word's high nibbles come out as 1024 + 16 u, their q is 1/16).  A group's accumulator starts at
-//            -sum_c q_c (1024 + 2^(b-1)), so it ends at sum_c q_c (u - 2^(b-1)); then S += scale[token][group] * it.
+// Every KV head's R = nodes * group rows of a sequence share its K and V, so a page (16 tokens) is read once for all of a
+// block's rows.  Two kernels: k_tree_mma, up to 24 rows a block, on warp-level matrix instructions (m16n8k16: 16 tokens
+// or 16 channels by 8 rows, so that a single row wastes an N of 8, not an M of 16 or 128), fed from registers; and
+// k_tree_tc, 128 rows a block, on tcgen05.
+//
+// k_tree_mma turns codes into operands without scaling them first:
+//   scores   S^T = K Q^T.  A code byte u under the fp16 exponent of 1024 is the number 1024 + u (one PRMT per two codes;
+//            4-bit codes in a word's high nibbles come out as 1024 + 16 u, their q is 1/16).  A group's accumulator starts
+//            at -sum_c q_c (1024 + 2^(b-1)), so it ends at sum_c q_c (u - 2^(b-1)); then S += scale[token][group] * it.
 //            |offset| is below 40 times the sum, whose fp32 rounding stays below 2^-17 of q's length times a code.
-//   values   the scale belongs to (token, group): the probabilities are multiplied by it (fp16, per group of 32
-//            channels) and the codes enter as exact integers (the offset taken off by one packed subtraction; it cannot
-//            be folded into the accumulator here, whose sum over thousands of tokens would cancel).
-// Channels within a group and tokens within a page may enter a contraction in any order, so each lane reads runs of
-// bytes: eight channels of a token for the scores, four channels of four tokens for the values, the tokens rotated by
-// the lane (tok()) so that a warp's reads touch every shared-memory bank once.
+//   values   Y^T = V^T P^T.  The scale belongs to (token, group): P, transposed by one movmatrix per 8 tokens, is multiplied
+//            by it in fp16, per group of 32 channels, and the codes enter as exact integers (the offset taken off by one
+//            packed subtraction; it cannot be folded into the accumulator here, whose sum over thousands of tokens would
+//            cancel).
+// Channels within a group may enter a contraction in any order, so each lane reads runs of bytes: eight channels of a
+// token for the scores, four channels of four tokens for the values.
 //
 // Running maximum and sum are per row in registers.  m is the row's maximum less 3 (log2 units) and moves only when a
 // score passes m + 7: p = 2^(s - m) <= 2^7, times a scale <= 258 stays inside fp16 (65504), while the largest weight
-// seen is at least 8, so that weights down to 2^-11 of it keep full precision even under small scales.
+// seen is at least 8, so that weights down to 2^-17 of it keep full precision.
 //
-// Work split: the units (sequence, KV head, block of 16 rows, page) of the whole call, in this order, are dealt to the
-// resident warps in equal runs; a warp writes one partial (m, l, Y) per row block that its run touches, and
-// k_tree_combine merges them.  Warps never wait for one another; each keeps its own ring of pages in flight with
-// 16-byte asynchronous copies.
+// Work split: the units (sequence, KV head, row block, page) of the whole call, in this order, are dealt to the resident
+// warps in equal runs; a warp writes one partial (m, l, Y) per row block that its run touches, and k_tree_combine
+// merges them.  Warps never wait for one another; each keeps its own ring of pages in flight with 16-byte
+// asynchronous copies.  (With 16 query rows as the M side instead, a page took 670 instructions, and 129 us for 16
+// sequences of 4K over 8 bits and 32 heads.)
 #include <float.h>
 
 #include "tc_common.cuh"
@@ -43,9 +46,15 @@ struct PageFmt {
   static constexpr int VS = BITS == 0 ? 0 : 128;                      // one head's value scales
   static constexpr int VB = BITS == 0 ? 4096 : 64 * 4 * BITS;         // one head's value codes
   static constexpr int STAGE = KB + VS + VB;                          // 8192, 4352 or 2304 bytes
-  // warps per SM: registers (two sets of query fragments for bf16) and 220 KB of shared memory
-  static constexpr int CTAS = BITS == 0 ? 2 : 3;
-  static constexpr int NS = BITS == 0 ? 3 : BITS == 8 ? 4 : 6;        // pages of a warp's ring
+};
+
+// Row blocks of 8 NT rows.  CTAs per SM by registers (16 NT + 32 NT of query fragments and sums; bf16 holds the queries as
+// two parts), ring stages by shared memory.
+template <int BITS, int NT>
+struct MmaFmt {
+  static constexpr int CTAS = BITS == 0 ? 2 : NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int NS = (int)(212 * 1024 / (CTAS * kTreeWarps) / PageFmt<BITS>::STAGE) < 8
+                                ? (int)(212 * 1024 / (CTAS * kTreeWarps) / PageFmt<BITS>::STAGE) : 8;
 };
 
 struct TreeWs {
@@ -215,15 +224,15 @@ __global__ void __launch_bounds__(128) k_tree_prep(TreeMma a) {
 }
 
 // ------------------------------------------------------------------ pieces of the main kernel
-__device__ __forceinline__ void mma_h(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_h(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, const float* c) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-__device__ __forceinline__ void mma_b(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_b(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, const float* c) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -242,6 +251,10 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
                             *reinterpret_cast<const __half2*>(&c));
@@ -257,22 +270,15 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Token of a page behind lane column j (0 .. 3), place i (0 .. 3).
-__device__ __forceinline__ int tok(int j, int i) { return 4 * j + ((i + j) & 3); }
-// bf16 pages: 16-byte chunk c of token t's 256-byte row is kept at chunk c ^ swz(t), so that the reads of both
-// contractions touch every bank once (row stride = two rounds of the banks).
-__device__ __forceinline__ int swz(int t) { return ((t & 1) << 2) | (t & 2); }
+// bf16 pages: 16-byte chunk c of token t's 256-byte row is kept at chunk c ^ swz(t): the rows of the eight lanes that read
+// together then start at different banks (row stride = two rounds of the banks).
+__device__ __forceinline__ int swz(int t) { return ((t & 1) << 2) | (t & 2) | ((t >> 2) & 1); }
 
-// The four scales of tokens 4 j .. 4 j + 3 (8 bytes at p) in the order tok(j, 0 .. 3).
-__device__ __forceinline__ void scales4(const uint8_t* p, uint32_t sel0, uint32_t sel1, float* s) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  const uint32_t r0 = __byte_perm(w.x, w.y, sel0), r1 = __byte_perm(w.x, w.y, sel1);
-  const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&r0));
-  const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&r1));
-  s[0] = f0.x;
-  s[1] = f0.y;
-  s[2] = f1.x;
-  s[3] = f1.y;
+// The 8 x 8 matrix of 16-bit elements whose rows r = lane / 4 hold columns 2 (lane % 4), + 1: transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 // Copies of one page of KV head g into a stage.
@@ -310,15 +316,16 @@ __device__ __forceinline__ void issue_page(const TreeMma& a, int page, int g, ui
   }
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(32 * kTreeWarps, PageFmt<BITS>::CTAS) k_tree_mma(TreeMma a) {
+template <int BITS, int NT>
+__global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tree_mma(TreeMma a) {
   using F = PageFmt<BITS>;
+  constexpr int NS = MmaFmt<BITS, NT>::NS, RB = 8 * NT, QP = BITS == 0 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t ring_all[];
   const LayerView& v = a.v;
   const TreeArgs& t = a.t;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, j = lane & 3;
-  uint8_t* ring = ring_all + (size_t)warp * F::NS * F::STAGE;
+  uint8_t* ring = ring_all + (size_t)warp * NS * F::STAGE;
   const uint32_t ring_s = tc::smem_u32(ring);
   const int GQ = v.group_q;
   const long long U = a.w.unit_off[t.batch];
@@ -327,76 +334,16 @@ __global__ void __launch_bounds__(32 * kTreeWarps, PageFmt<BITS>::CTAS) k_tree_m
   if (w >= We) return;
   long long u = (long long)w * U / We;
   const long long u1 = (long long)(w + 1) * U / We;
-  // selectors that rotate four fp16 numbers by j places
-  uint32_t sel0, sel1;
-  {
-    const uint32_t c0 = 2 * j, c1 = 2 * ((j + 1) & 3), c2 = 2 * ((j + 2) & 3), c3 = 2 * ((j + 3) & 3);
-    sel0 = c0 | (c0 + 1) << 4 | c1 << 8 | (c1 + 1) << 12;
-    sel1 = c2 | (c2 + 1) << 4 | c3 << 8 | (c3 + 1) << 12;
-  }
   while (u < u1) {
     // ---- the row block of unit u
     const int b = warp_find(a.w.unit_off, t.batch, u, lane);
     const TreeSeq sq = seq_of(t, b, v.status, false);
-    const int R = sq.cnt * GQ, nrb = (R + 15) / 16, len = sq.hist + sq.cnt, pages = (len + kPage - 1) / kPage;
+    const int R = sq.cnt * GQ, nrb = (R + RB - 1) / RB, len = sq.hist + sq.cnt, pages = (len + kPage - 1) / kPage;
     const long long rem = u - a.w.unit_off[b];
     const int blk = (int)(rem / pages), p0 = (int)(rem % pages);
     const int g = blk / nrb, rb = blk % nrb;
     const int p1 = (int)min((long long)pages, p0 + (u1 - u));
     const int32_t* pt = t.pt + (size_t)b * t.max_pages;
-    // ---- query fragments: rows r and r + 8 of the block, channels 32 g' + 8 j ..
-    uint32_t qa[BITS == 0 ? 16 : 8][4];
-    const int row0 = rb * 16 + r, row1 = row0 + 8;
-    const int node0 = row0 / GQ, node1 = row1 / GQ;
-    {
-      const uint4* q0 = reinterpret_cast<const uint4*>((const uint16_t*)a.w.q +
-                                                       ((size_t)(sq.off + node0) * v.H + g * GQ + row0 % GQ) * 128);
-      const uint4* q1 = reinterpret_cast<const uint4*>((const uint16_t*)a.w.q +
-                                                       ((size_t)(sq.off + node1) * v.H + g * GQ + row1 % GQ) * 128);
-#pragma unroll
-      for (int part = 0; part < (BITS == 0 ? 2 : 1); ++part) {
-        const size_t o = (size_t)part * t.n_nodes * v.H * 16;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 x = row0 < R ? q0[o + 4 * c + j] : make_uint4(0, 0, 0, 0);
-          const uint4 y = row1 < R ? q1[o + 4 * c + j] : make_uint4(0, 0, 0, 0);
-          uint32_t* f0 = qa[part * 8 + 2 * c];
-          uint32_t* f1 = qa[part * 8 + 2 * c + 1];
-          f0[0] = x.x; f0[1] = y.x; f0[2] = x.y; f0[3] = y.y;
-          f1[0] = x.z; f1[1] = y.z; f1[2] = x.w; f1[3] = y.w;
-        }
-      }
-    }
-    // a group's accumulator starts at minus the part of the sum that the codes' offset makes
-    float bias0[4], bias1[4];
-    if constexpr (BITS != 0) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qa[2 * c + k][e]));
-            // 4-bit: elements 2, 3 of a fragment (high nibbles) meet 1024 + 16 u
-            const float z = BITS == 8 ? 1152.f : (e & 2) ? 1152.f : 1032.f;
-            ((e & 1) ? s1 : s0) -= (f.x + f.y) * z;
-          }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-          s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-        }
-        bias0[c] = s0;
-        bias1[c] = s1;
-      }
-    }
-    float Y[16][4];
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) Y[k][e] = 0.f;
-    float m0 = -1e30f, m1 = -1e30f, l0 = 0.f, l1 = 0.f;
     // ---- pages p0 .. p1, NS - 1 ahead
     int ids = p0 + lane < p1 ? pt[p0 + lane] : 0, ids0 = p0;
     int next = p0;
@@ -407,191 +354,306 @@ __global__ void __launch_bounds__(32 * kTreeWarps, PageFmt<BITS>::CTAS) k_tree_m
           ids = ids0 + lane < p1 ? pt[ids0 + lane] : 0;
         }
         const int page = __shfl_sync(0xffffffffu, ids, next - ids0);
-        issue_page<BITS>(a, page, g, ring_s + (uint32_t)((next - p0) % F::NS) * F::STAGE, lane);
+        issue_page<BITS>(a, page, g, ring_s + (uint32_t)((next - p0) % NS) * F::STAGE, lane);
         ++next;
       }
       cp_commit();
     };
+#pragma unroll 1
+    for (int k = 0; k < NS - 1; ++k) issue();
+    // ---- query fragments (the N side): row 8 n + r, channels 32 c + 8 j ..
+    uint32_t qf[QP][NT][8][2];
 #pragma unroll
-    for (int k = 0; k < F::NS - 1; ++k) issue();
+    for (int n = 0; n < NT; ++n) {
+      const int row = rb * RB + 8 * n + r;
+      const uint4* q = reinterpret_cast<const uint4*>((const uint16_t*)a.w.q +
+                                                      ((size_t)(sq.off + row / GQ) * v.H + g * GQ + row % GQ) * 128);
+#pragma unroll
+      for (int part = 0; part < QP; ++part) {
+        const size_t o = (size_t)part * t.n_nodes * v.H * 16;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 x = row < R ? q[o + 4 * c + j] : make_uint4(0, 0, 0, 0);
+          qf[part][n][2 * c][0] = x.x;
+          qf[part][n][2 * c][1] = x.y;
+          qf[part][n][2 * c + 1][0] = x.z;
+          qf[part][n][2 * c + 1][1] = x.w;
+        }
+      }
+    }
+    // a group's accumulator starts at minus the part of the sum that the codes' offset makes (rows 8 n + 2 j, + 1)
+    float bias[NT][4][2];
+    if constexpr (BITS != 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float s = 0.f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[0][n][2 * c + k][e]));
+              // 4-bit: the second register of a step (high nibbles) meets 1024 + 16 u
+              s -= (f.x + f.y) * (BITS == 8 || e == 1 ? 1152.f : 1032.f);
+            }
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          bias[n][c][0] = __shfl_sync(0xffffffffu, s, 8 * j);
+          bias[n][c][1] = __shfl_sync(0xffffffffu, s, 8 * j + 4);
+        }
+    }
+    float Y[NT][8][4];   // m-tile 2 c + i: rows r, r + 8 = channels 32 c + 4 r + 2 i, + 1; columns: query rows 2 j, + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Y[n][k][e] = 0.f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -1e30f;
+      l[n][0] = l[n][1] = 0.f;
+    }
+    int slot = 0;
+#pragma unroll 1
     for (int p = p0; p < p1; ++p) {
-      cp_wait<F::NS - 2>();
+      cp_wait<NS - 2>();
       __syncwarp();   // this page's bytes from every lane; every lane is done with the stage that is filled next
       issue();
-      const uint8_t* st = ring + (size_t)((p - p0) % F::NS) * F::STAGE;
-      // ---- scores of 16 tokens: S[tl] columns 2 j, 2 j + 1 = tokens tok(j, 2 tl), tok(j, 2 tl + 1)
-      float S[2][4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[0][e] = S[1][e] = 0.f;
-      const int kn = r >> 1, ki = r & 1;   // operand column r of tile tl is token tok(r / 2, r % 2 + 2 tl)
+      const uint8_t* st = ring + slot * F::STAGE;
+      slot = slot + 1 == NS ? 0 : slot + 1;
+      // ---- scores of 16 tokens: S[n] rows r, r + 8 = tokens, columns = query rows 8 n + 2 j, + 1
+      float S[NT][4];
       if constexpr (BITS == 0) {
 #pragma unroll
-        for (int tl = 0; tl < 2; ++tl) {
-          const int kt = tok(kn, ki + 2 * tl);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(st + kt * 256 + (((4 * c + j) ^ swz(kt)) << 4));
-            mma_b(S[tl], qa[2 * c], x.x, x.y);
-            mma_b(S[tl], qa[2 * c + 1], x.z, x.w);
-            mma_b(S[tl], qa[8 + 2 * c], x.x, x.y);
-            mma_b(S[tl], qa[8 + 2 * c + 1], x.z, x.w);
-          }
+          for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(st + r * 256 + (((4 * c + j) ^ swz(r)) << 4));
+          const uint4 y = *reinterpret_cast<const uint4*>(st + (r + 8) * 256 + (((4 * c + j) ^ swz(r + 8)) << 4));
+          const uint32_t k0[4] = {x.x, y.x, x.y, y.y}, k1[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+          for (int part = 0; part < QP; ++part)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_b(S[n], k0, qf[part][n][2 * c][0], qf[part][n][2 * c][1], S[n]);
+              mma_b(S[n], k1, qf[part][n][2 * c + 1][0], qf[part][n][2 * c + 1][1], S[n]);
+            }
         }
       } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float sc[4];
-          scales4(st + c * 32 + j * 8, sel0, sel1, sc);
+          const float s0 = __half2float(*reinterpret_cast<const __half*>(st + c * 32 + r * 2));
+          const float s1 = __half2float(*reinterpret_cast<const __half*>(st + c * 32 + 16 + r * 2));
+          uint32_t k0[4], k1[4];
+          if constexpr (BITS == 8) {
+            constexpr uint32_t ex = 0x64646464u;
+            const uint2 x = *reinterpret_cast<const uint2*>(st + 128 + c * 512 + r * 32 + j * 8);
+            const uint2 y = *reinterpret_cast<const uint2*>(st + 128 + c * 512 + 256 + r * 32 + j * 8);
+            k0[0] = __byte_perm(x.x, ex, 0x4140);
+            k0[1] = __byte_perm(y.x, ex, 0x4140);
+            k0[2] = __byte_perm(x.x, ex, 0x4342);
+            k0[3] = __byte_perm(y.x, ex, 0x4342);
+            k1[0] = __byte_perm(x.y, ex, 0x4140);
+            k1[1] = __byte_perm(y.y, ex, 0x4140);
+            k1[2] = __byte_perm(x.y, ex, 0x4342);
+            k1[3] = __byte_perm(y.y, ex, 0x4342);
+          } else {
+            constexpr uint32_t lm = 0x000F000Fu, hm = 0x00F000F0u, ex = 0x64006400u;
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(st + 128 + c * 256 + r * 16 + j * 4);
+            const uint32_t y = *reinterpret_cast<const uint32_t*>(st + 128 + c * 256 + 128 + r * 16 + j * 4);
+            k0[0] = (x & lm) | ex;
+            k0[1] = (y & lm) | ex;
+            k0[2] = (x & hm) | ex;
+            k0[3] = (y & hm) | ex;
+            k1[0] = ((x >> 8) & lm) | ex;
+            k1[1] = ((y >> 8) & lm) | ex;
+            k1[2] = ((x >> 8) & hm) | ex;
+            k1[3] = ((y >> 8) & hm) | ex;
+          }
 #pragma unroll
-          for (int tl = 0; tl < 2; ++tl) {
-            const int kt = tok(kn, ki + 2 * tl);
-            float acc[4] = {bias0[c], bias0[c], bias1[c], bias1[c]};
-            if constexpr (BITS == 8) {
-              const uint2 x = *reinterpret_cast<const uint2*>(st + 128 + c * 512 + kt * 32 + j * 8);
-              mma_h(acc, qa[2 * c], __byte_perm(x.x, 0x64646464u, 0x4140), __byte_perm(x.x, 0x64646464u, 0x4342));
-              mma_h(acc, qa[2 * c + 1], __byte_perm(x.y, 0x64646464u, 0x4140), __byte_perm(x.y, 0x64646464u, 0x4342));
+          for (int n = 0; n < NT; ++n) {
+            const float start[4] = {bias[n][c][0], bias[n][c][1], bias[n][c][0], bias[n][c][1]};
+            float acc[4];
+            mma_h(acc, k0, qf[0][n][2 * c][0], qf[0][n][2 * c][1], start);
+            mma_h(acc, k1, qf[0][n][2 * c + 1][0], qf[0][n][2 * c + 1][1], acc);
+            if (c == 0) {
+              S[n][0] = s0 * acc[0];
+              S[n][1] = s0 * acc[1];
+              S[n][2] = s1 * acc[2];
+              S[n][3] = s1 * acc[3];
             } else {
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(st + 128 + c * 256 + kt * 16 + j * 4);
-              const uint32_t x8 = x >> 8;
-              mma_h(acc, qa[2 * c], (x & 0x000F000Fu) | 0x64006400u, (x & 0x00F000F0u) | 0x64006400u);
-              mma_h(acc, qa[2 * c + 1], (x8 & 0x000F000Fu) | 0x64006400u, (x8 & 0x00F000F0u) | 0x64006400u);
+              S[n][0] += s0 * acc[0];
+              S[n][1] += s0 * acc[1];
+              S[n][2] += s1 * acc[2];
+              S[n][3] += s1 * acc[3];
             }
-            S[tl][0] += sc[2 * tl] * acc[0];
-            S[tl][1] += sc[2 * tl + 1] * acc[1];
-            S[tl][2] += sc[2 * tl] * acc[2];
-            S[tl][3] += sc[2 * tl + 1] * acc[3];
           }
         }
       }
       const bool tail = p * kPage + kPage > sq.hist;   // the page holds drafted nodes or unused slots
       if (tail) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = p * kPage + tok(j, i) - sq.hist;   // node of this slot (negative: history)
-          bool s0 = x < 0, s1 = s0;
-          if (x >= 0 && x < sq.cnt) {
-            if (row0 < R) s0 = tree_sees(t.mask, t.mask_words, sq.off + node0, node0, x);
-            if (row1 < R) s1 = tree_sees(t.mask, t.mask_words, sq.off + node1, node1, x);
+#pragma unroll 1
+        for (int x = 0; x < 2 * NT; ++x) {   // query row 8 (x / 2) + 2 j + x % 2, tokens r and r + 8
+          const int row = rb * RB + 8 * (x >> 1) + 2 * j + (x & 1), node = row / GQ;
+          const int k0 = p * kPage + r - sq.hist, k1 = k0 + 8;   // nodes of the slots (negative: history)
+          bool v0 = k0 < 0, v1 = k1 < 0;
+          if (row < R) {
+            if (k0 >= 0 && k0 < sq.cnt) v0 = tree_sees(t.mask, t.mask_words, sq.off + node, node, k0);
+            if (k1 >= 0 && k1 < sq.cnt) v1 = tree_sees(t.mask, t.mask_words, sq.off + node, node, k1);
           }
-          if (!s0) S[i >> 1][i & 1] = -INFINITY;
-          if (!s1) S[i >> 1][2 + (i & 1)] = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (x == 2 * n + e) {
+                if (!v0) S[n][e] = -INFINITY;
+                if (!v1) S[n][2 + e] = -INFINITY;
+              }
         }
       }
       // ---- running maximum
-      const float x0 = fmaxf(fmaxf(S[0][0], S[0][1]), fmaxf(S[1][0], S[1][1]));
-      const float x1 = fmaxf(fmaxf(S[0][2], S[0][3]), fmaxf(S[1][2], S[1][3]));
-      if (__any_sync(0xffffffffu, x0 > m0 + 7.f || x1 > m1 + 7.f)) {
-        float y0 = x0, y1 = x1;
+      bool up = false;
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, o));
-          y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
-        }
-        const float n0 = fmaxf(m0, y0 - 3.f), n1 = fmaxf(m1, y1 - 3.f);
-        const float f0 = ex2(m0 - n0), f1 = ex2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= f0;
-        l1 *= f1;
+      for (int n = 0; n < NT; ++n)
+        up = up || fmaxf(S[n][0], S[n][2]) > m[n][0] + 7.f || fmaxf(S[n][1], S[n][3]) > m[n][1] + 7.f;
+      if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          Y[k][0] *= f0;
-          Y[k][1] *= f0;
-          Y[k][2] *= f1;
-          Y[k][3] *= f1;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = fmaxf(S[n][e], S[n][2 + e]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+            const float mn = fmaxf(m[n][e], y - 3.f), f = ex2(m[n][e] - mn);
+            m[n][e] = mn;
+            l[n][e] *= f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              Y[n][k][e] *= f;
+              Y[n][k][2 + e] *= f;
+            }
+          }
+      }
+      // ---- P (tokens r, r + 8 by query rows 2 j, + 1), transposed into the operand of the values: tokens 2 j .., row r
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float e0 = ex2(S[n][0] - m[n][0]), e1 = ex2(S[n][1] - m[n][1]);
+        const float e2 = ex2(S[n][2] - m[n][0]), e3 = ex2(S[n][3] - m[n][1]);
+        if constexpr (BITS == 0) {
+          const uint32_t x = b2(e0, e1), y = b2(e2, e3);
+          // the sum is over the rounded weights, so that they add up to one
+          l[n][0] += __uint_as_float(x << 16) + __uint_as_float(y << 16);
+          l[n][1] += __uint_as_float(x & 0xFFFF0000u) + __uint_as_float(y & 0xFFFF0000u);
+          pb[n][0] = transpose8(x);
+          pb[n][1] = transpose8(y);
+        } else {
+          l[n][0] += e0 + e2;
+          l[n][1] += e1 + e3;
+          pb[n][0] = transpose8(h2(e0, e1));
+          pb[n][1] = transpose8(h2(e2, e3));
         }
       }
-      float P[4][2];   // [token place i][row]
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        P[i][0] = ex2(S[i >> 1][i & 1] - m0);
-        P[i][1] = ex2(S[i >> 1][2 + (i & 1)] - m1);
-      }
-      // ---- values
+      // ---- values: tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9, channels 32 c + 4 r .. + 3
       if constexpr (BITS == 0) {
         const uint8_t* sv = st + F::KB;
-        uint32_t pa[4] = {b2(P[0][0], P[1][0]), b2(P[0][1], P[1][1]), b2(P[2][0], P[3][0]), b2(P[2][1], P[3][1])};
-        // the sum is over the rounded weights, so that they add up to one
-        auto lo16 = [](uint32_t x) { return __uint_as_float(x << 16); };
-        auto hi16 = [](uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); };
-        l0 += (lo16(pa[0]) + hi16(pa[0])) + (lo16(pa[2]) + hi16(pa[2]));
-        l1 += (lo16(pa[1]) + hi16(pa[1])) + (lo16(pa[3]) + hi16(pa[3]));
-        unsigned bad = 0;   // place i of this lane's tokens holds an infinity or a NaN
+        unsigned bad = 0;   // bit t: token t holds an infinity or a NaN (among this lane's bytes)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint2 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int vt = tok(j, i);
+            const int vt = 2 * j + (i & 1) + 8 * (i >> 1);
             x[i] = *reinterpret_cast<const uint2*>(sv + vt * 256 + (((4 * c + (r >> 1)) ^ swz(vt)) << 4) + (r & 1) * 8);
             if (tail) {
               // a slot that some rows do not see must not reach them through 0 * NaN: it enters as zero, and the rows
               // that do see it become NaN below
               auto odd = [](uint32_t y) { return (y & 0x7F80u) == 0x7F80u || (y & 0x7F800000u) == 0x7F800000u; };
               if (odd(x[i].x) || odd(x[i].y)) {
-                bad |= 1u << i;
+                bad |= 1u << vt;
                 x[i] = make_uint2(0u, 0u);
               }
             }
           }
-          mma_b(Y[4 * c + 0], pa, __byte_perm(x[0].x, x[1].x, 0x5410), __byte_perm(x[2].x, x[3].x, 0x5410));
-          mma_b(Y[4 * c + 1], pa, __byte_perm(x[0].x, x[1].x, 0x7632), __byte_perm(x[2].x, x[3].x, 0x7632));
-          mma_b(Y[4 * c + 2], pa, __byte_perm(x[0].y, x[1].y, 0x5410), __byte_perm(x[2].y, x[3].y, 0x5410));
-          mma_b(Y[4 * c + 3], pa, __byte_perm(x[0].y, x[1].y, 0x7632), __byte_perm(x[2].y, x[3].y, 0x7632));
+          const uint32_t v0[4] = {__byte_perm(x[0].x, x[1].x, 0x5410), __byte_perm(x[0].x, x[1].x, 0x7632),
+                                  __byte_perm(x[2].x, x[3].x, 0x5410), __byte_perm(x[2].x, x[3].x, 0x7632)};
+          const uint32_t v1[4] = {__byte_perm(x[0].y, x[1].y, 0x5410), __byte_perm(x[0].y, x[1].y, 0x7632),
+                                  __byte_perm(x[2].y, x[3].y, 0x5410), __byte_perm(x[2].y, x[3].y, 0x7632)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_b(Y[n][2 * c], v0, pb[n][0], pb[n][1], Y[n][2 * c]);
+            mma_b(Y[n][2 * c + 1], v1, pb[n][0], pb[n][1], Y[n][2 * c + 1]);
+          }
         }
         if (tail) {
+          bad = __reduce_or_sync(0xffffffffu, bad);
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (bad >> i & 1) {
-              if (S[i >> 1][i & 1] != -INFINITY) l0 = NAN;
-              if (S[i >> 1][2 + (i & 1)] != -INFINITY) l1 = NAN;
+            for (int e = 0; e < 2; ++e) {
+              if ((bad >> r & 1u) && S[n][e] != -INFINITY) l[n][e] = NAN;
+              if ((bad >> (r + 8) & 1u) && S[n][2 + e] != -INFINITY) l[n][e] = NAN;
             }
         }
       } else {
-        l0 += (P[0][0] + P[1][0]) + (P[2][0] + P[3][0]);
-        l1 += (P[0][1] + P[1][1]) + (P[2][1] + P[3][1]);
         const uint8_t* sv = st + F::KB;
         const uint8_t* cv = sv + F::VS;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float sc[4];
-          scales4(sv + c * 32 + j * 8, sel0, sel1, sc);
+          uint32_t sc0 = *reinterpret_cast<const uint32_t*>(sv + c * 32 + j * 4);        // scales of tokens 2 j, 2 j + 1
+          uint32_t sc1 = *reinterpret_cast<const uint32_t*>(sv + c * 32 + 16 + j * 4);   // and 8 on
           if (tail) {
             // unused slots may hold any bytes: no scale that is not a number meets a weight of zero
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (p * kPage + tok(j, i) >= len) sc[i] = 0.f;
+            const int n0 = len - p * kPage - 2 * j, n1 = n0 - 8;   // tokens of the pair on
+            sc0 = n0 >= 2 ? sc0 : n0 == 1 ? sc0 & 0xFFFFu : 0u;
+            sc1 = n1 >= 2 ? sc1 : n1 == 1 ? sc1 & 0xFFFFu : 0u;
           }
-          const uint32_t pa[4] = {h2(P[0][0] * sc[0], P[1][0] * sc[1]), h2(P[0][1] * sc[0], P[1][1] * sc[1]),
-                                  h2(P[2][0] * sc[2], P[3][0] * sc[3]), h2(P[2][1] * sc[2], P[3][1] * sc[3])};
+          uint32_t v0[4], v1[4];
           if constexpr (BITS == 8) {
             uint32_t x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              x[i] = *reinterpret_cast<const uint32_t*>(cv + c * 512 + tok(j, i) * 32 + r * 4);
+              x[i] = *reinterpret_cast<const uint32_t*>(cv + c * 512 + (2 * j + (i & 1) + 8 * (i >> 1)) * 32 + r * 4);
             const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), b01 = __byte_perm(x[0], x[1], 0x7362);
             const uint32_t a23 = __byte_perm(x[2], x[3], 0x5140), b23 = __byte_perm(x[2], x[3], 0x7362);
             constexpr uint32_t off = 0x64806480u, ex = 0x64646464u;   // 1152, 1152
-            mma_h(Y[4 * c + 0], pa, hsub2(__byte_perm(a01, ex, 0x4140), off), hsub2(__byte_perm(a23, ex, 0x4140), off));
-            mma_h(Y[4 * c + 1], pa, hsub2(__byte_perm(a01, ex, 0x4342), off), hsub2(__byte_perm(a23, ex, 0x4342), off));
-            mma_h(Y[4 * c + 2], pa, hsub2(__byte_perm(b01, ex, 0x4140), off), hsub2(__byte_perm(b23, ex, 0x4140), off));
-            mma_h(Y[4 * c + 3], pa, hsub2(__byte_perm(b01, ex, 0x4342), off), hsub2(__byte_perm(b23, ex, 0x4342), off));
+            v0[0] = hsub2(__byte_perm(a01, ex, 0x4140), off);
+            v0[1] = hsub2(__byte_perm(a01, ex, 0x4342), off);
+            v0[2] = hsub2(__byte_perm(a23, ex, 0x4140), off);
+            v0[3] = hsub2(__byte_perm(a23, ex, 0x4342), off);
+            v1[0] = hsub2(__byte_perm(b01, ex, 0x4140), off);
+            v1[1] = hsub2(__byte_perm(b01, ex, 0x4342), off);
+            v1[2] = hsub2(__byte_perm(b23, ex, 0x4140), off);
+            v1[3] = hsub2(__byte_perm(b23, ex, 0x4342), off);
           } else {
             uint32_t x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              x[i] = *reinterpret_cast<const uint16_t*>(cv + c * 256 + tok(j, i) * 16 + r * 2);
+              x[i] = *reinterpret_cast<const uint16_t*>(cv + c * 256 + (2 * j + (i & 1) + 8 * (i >> 1)) * 16 + r * 2);
             const uint32_t w01 = __byte_perm(x[0], x[1], 0x5410), w23 = __byte_perm(x[2], x[3], 0x5410);
+            const uint32_t h01 = w01 >> 8, h23 = w23 >> 8;
             constexpr uint32_t lm = 0x000F000Fu, hm = 0x00F000F0u, ex = 0x64006400u;
             constexpr uint32_t off = 0x64086408u;                       // 1032
             constexpr uint32_t s16 = 0x2C002C00u, o16 = 0xD480D480u;    // 1/16, -72
-            mma_h(Y[4 * c + 0], pa, hsub2((w01 & lm) | ex, off), hsub2((w23 & lm) | ex, off));
-            mma_h(Y[4 * c + 1], pa, hfma2((w01 & hm) | ex, s16, o16), hfma2((w23 & hm) | ex, s16, o16));
-            const uint32_t h01 = w01 >> 8, h23 = w23 >> 8;
-            mma_h(Y[4 * c + 2], pa, hsub2((h01 & lm) | ex, off), hsub2((h23 & lm) | ex, off));
-            mma_h(Y[4 * c + 3], pa, hfma2((h01 & hm) | ex, s16, o16), hfma2((h23 & hm) | ex, s16, o16));
+            v0[0] = hsub2((w01 & lm) | ex, off);
+            v0[1] = hfma2((w01 & hm) | ex, s16, o16);
+            v0[2] = hsub2((w23 & lm) | ex, off);
+            v0[3] = hfma2((w23 & hm) | ex, s16, o16);
+            v1[0] = hsub2((h01 & lm) | ex, off);
+            v1[1] = hfma2((h01 & hm) | ex, s16, o16);
+            v1[2] = hsub2((h23 & lm) | ex, off);
+            v1[3] = hfma2((h23 & hm) | ex, s16, o16);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t ps0 = hmul2(pb[n][0], sc0), ps1 = hmul2(pb[n][1], sc1);
+            mma_h(Y[n][2 * c], v0, ps0, ps1, Y[n][2 * c]);
+            mma_h(Y[n][2 * c + 1], v1, ps0, ps1, Y[n][2 * c + 1]);
           }
         }
       }
@@ -599,31 +661,27 @@ __global__ void __launch_bounds__(32 * kTreeWarps, PageFmt<BITS>::CTAS) k_tree_m
     cp_wait<0>();
     __syncwarp();
     // ---- the partial of this row block
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-    }
     const long long part = a.w.item_off[b] + blk + w;
-    if (j == 0) {
-      a.w.pm[part * 16 + r] = m0;
-      a.w.pm[part * 16 + r + 8] = m1;
-      a.w.pl[part * 16 + r] = l0;
-      a.w.pl[part * 16 + r + 8] = l1;
-    }
-    float* y0 = a.w.pY + (part * 16 + r) * 128 + 8 * j;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      // tile 4 c + i: columns 2 j, 2 j + 1 = channels 32 c + 8 j + i, + 4
-      if (row0 < R) {
-        *reinterpret_cast<float4*>(y0 + 32 * c) = make_float4(Y[4 * c][0], Y[4 * c + 1][0], Y[4 * c + 2][0], Y[4 * c + 3][0]);
-        *reinterpret_cast<float4*>(y0 + 32 * c + 4) = make_float4(Y[4 * c][1], Y[4 * c + 1][1], Y[4 * c + 2][1], Y[4 * c + 3][1]);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float s = l[n][e];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const int q = 8 * n + 2 * j + e;
+        if (r == 0) {
+          a.w.pm[part * RB + q] = m[n][e];
+          a.w.pl[part * RB + q] = s;
+        }
+        if (rb * RB + q < R) {
+          float* y = a.w.pY + (part * RB + q) * 128 + 4 * r;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<float4*>(y + 32 * c) =
+                make_float4(Y[n][2 * c][e], Y[n][2 * c][2 + e], Y[n][2 * c + 1][e], Y[n][2 * c + 1][2 + e]);
+        }
       }
-      if (row1 < R) {
-        *reinterpret_cast<float4*>(y0 + 1024 + 32 * c) = make_float4(Y[4 * c][2], Y[4 * c + 1][2], Y[4 * c + 2][2], Y[4 * c + 3][2]);
-        *reinterpret_cast<float4*>(y0 + 1024 + 32 * c + 4) = make_float4(Y[4 * c][3], Y[4 * c + 1][3], Y[4 * c + 2][3], Y[4 * c + 3][3]);
-      }
-    }
     u += p1 - p0;
   }
 }
@@ -784,25 +842,21 @@ __device__ __forceinline__ void tmem_st32x(uint32_t taddr, const uint32_t* v) {
 // it too; the output is put in order where it leaves TMEM).
 template <int BITS>
 __device__ __forceinline__ uint4 deq8(uint2 w, uint32_t s2) {
-  auto hmul = [](uint32_t x, uint32_t y) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  };
   uint32_t o[4];
   if constexpr (BITS == 8) {
     constexpr uint32_t off = 0x64806480u, ex = 0x64646464u;
-    o[0] = hmul(hsub2(__byte_perm(w.x, ex, 0x4140), off), s2);
-    o[1] = hmul(hsub2(__byte_perm(w.x, ex, 0x4342), off), s2);
-    o[2] = hmul(hsub2(__byte_perm(w.y, ex, 0x4140), off), s2);
-    o[3] = hmul(hsub2(__byte_perm(w.y, ex, 0x4342), off), s2);
+    o[0] = hmul2(hsub2(__byte_perm(w.x, ex, 0x4140), off), s2);
+    o[1] = hmul2(hsub2(__byte_perm(w.x, ex, 0x4342), off), s2);
+    o[2] = hmul2(hsub2(__byte_perm(w.y, ex, 0x4140), off), s2);
+    o[3] = hmul2(hsub2(__byte_perm(w.y, ex, 0x4342), off), s2);
   } else {
     const uint32_t x = w.x, x8 = w.x >> 8;
     constexpr uint32_t lm = 0x000F000Fu, hm = 0x00F000F0u, ex = 0x64006400u, off = 0x64086408u;
     constexpr uint32_t s16 = 0x2C002C00u, o16 = 0xD480D480u;
-    o[0] = hmul(hsub2((x & lm) | ex, off), s2);
-    o[1] = hmul(hfma2((x & hm) | ex, s16, o16), s2);
-    o[2] = hmul(hsub2((x8 & lm) | ex, off), s2);
-    o[3] = hmul(hfma2((x8 & hm) | ex, s16, o16), s2);
+    o[0] = hmul2(hsub2((x & lm) | ex, off), s2);
+    o[1] = hmul2(hfma2((x & hm) | ex, s16, o16), s2);
+    o[2] = hmul2(hsub2((x8 & lm) | ex, off), s2);
+    o[3] = hmul2(hfma2((x8 & hm) | ex, s16, o16), s2);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -1186,32 +1240,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
 }
 
 // ------------------------------------------------------------------ merging the partials
-// One warp per (output row, query head), lane: four channels.  Writes y as fp16 into the output product's B tiles;
-// rows of no sequence and the tiles' padding rows are zero.
-__global__ void __launch_bounds__(256) k_tree_combine(TreeMma a, int rows_pad, int NB, int KT) {
+// One warp per output row and `hpw` query heads of it, lane: four channels.  Writes y as fp16 into the output product's B
+// tiles; rows of no sequence and the tiles' padding rows are zero.
+__global__ void __launch_bounds__(256) k_tree_combine(TreeMma a, int rows_pad, int NB, int KT, int hpw) {
   const LayerView& v = a.v;
   const TreeArgs& t = a.t;
   const int lane = threadIdx.x & 31;
   const long long id = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-  if (id >= (long long)rows_pad * v.H) return;
-  const int row = (int)(id / v.H), h = (int)(id % v.H);
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int parts = (v.H + hpw - 1) / hpw;
+  if (id >= (long long)rows_pad * parts) return;
+  const int row = (int)(id / parts), h0 = (int)(id % parts) * hpw;
   int b = -1;
   if (t.lens)
     b = row < t.batch ? row : -1;
   else if (row >= t.node_off[0] && row < t.node_off[t.batch])
     b = warp_find(t.node_off, t.batch, row, lane);
-  if (b >= 0) {
-    const TreeSeq sq = seq_of(t, b, v.status, false);
-    if (sq.cnt > 0 && row >= sq.off && row - sq.off < sq.cnt && a.w.item_off[b + 1] > a.w.item_off[b]) {
+  TreeSeq sq{0, 0, 0, 0};
+  if (b >= 0) sq = seq_of(t, b, v.status, false);
+  const bool live = sq.cnt > 0 && row >= sq.off && row - sq.off < sq.cnt && a.w.item_off[b + 1] > a.w.item_off[b];
+  const int nrb = (sq.cnt * v.group_q + a.rb - 1) / a.rb, units = (sq.hist + sq.cnt + a.unit - 1) / a.unit;
+  const long long U = a.w.unit_off[t.batch], We = workers_used(a, U);
+  const long long u0 = live ? a.w.unit_off[b] : 0, i0 = live ? a.w.item_off[b] : 0;
+  const int nt = row / NB, br = row % NB;
+  for (int h = h0; h < min(v.H, h0 + hpw); ++h) {
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
       const int g = h / v.group_q, rr = (row - sq.off) * v.group_q + h % v.group_q;
-      const int nrb = (sq.cnt * v.group_q + a.rb - 1) / a.rb, units = (sq.hist + sq.cnt + a.unit - 1) / a.unit;
       const int blk = g * nrb + rr / a.rb, r = rr % a.rb;
-      const long long U = a.w.unit_off[t.batch];
-      const long long We = workers_used(a, U);
-      const long long lo = a.w.unit_off[b] + (long long)blk * units, hi = lo + units - 1;
+      const long long lo = u0 + (long long)blk * units, hi = lo + units - 1;
       const long long w0 = ((lo + 1) * We - 1) / U, w1 = ((hi + 1) * We - 1) / U;   // the warps of the first, last unit
-      const long long base = a.w.item_off[b] + blk;
+      const long long base = i0 + blk;
       float m = -FLT_MAX, l = 0.f;
       for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, a.w.pm[(base + w) * a.rb + r]);
 #pragma unroll
@@ -1230,39 +1288,44 @@ __global__ void __launch_bounds__(256) k_tree_combine(TreeMma a, int rows_pad, i
       const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: zero; NaN stays
       y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
     }
+    const uint32_t k = (uint32_t)(h * 128 + lane * 4), c = k & 63u;
+    uint8_t* tile = (uint8_t*)a.w.y + ((size_t)nt * KT + (k >> 6)) * (size_t)NB * 128;
+    *reinterpret_cast<uint2*>(tile + tc::sw128((uint32_t)br, c >> 3) + (c & 7u) * 2u) = make_uint2(h2(y.x, y.y), h2(y.z, y.w));
   }
-  const int nt = row / NB, br = row % NB;
-  const uint32_t k = (uint32_t)(h * 128 + lane * 4), c = k & 63u;
-  uint8_t* tile = (uint8_t*)a.w.y + ((size_t)nt * KT + (k >> 6)) * (size_t)NB * 128;
-  *reinterpret_cast<uint2*>(tile + tc::sw128((uint32_t)br, c >> 3) + (c & 7u) * 2u) = make_uint2(h2(y.x, y.y), h2(y.z, y.w));
 }
 
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
-int tree_workers(int kv_bits) {
-  const int per_sm = (kv_bits == 0 ? PageFmt<0>::CTAS : PageFmt<8>::CTAS) * kTreeWarps;
-  return per_sm * num_sms();
-}
+template <int BITS, int NT>
+int mma_workers() { return MmaFmt<BITS, NT>::CTAS * kTreeWarps * num_sms(); }
 
 struct TreePlan {
   size_t unit_off, item_off, q, pm, pl, pY, y, part, total;
   int NB, rows_pad;
   bool tc;               // k_tree_tc
-  int workers, rb;
+  bool full;             // output product by 128 x 128 tiles, not stream-K
+  int workers, rb, nt;   // nt: 8-row tiles of a row block of k_tree_mma
 };
 
 // Rows per sequence and KV head from which the 128-row kernel is taken.
-constexpr int kTcFrom = 33;
+constexpr int kTcFrom = 25;
 
 TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
   const LayerView& v = L->view;
   TreePlan p;
-  p.NB = outproj_nb(n_nodes);
+  // Up to 256 rows the output product reads W_o once in an even split over the SMs; beyond, 128 x 128 tiles fill them.
+  p.full = n_nodes > 256;
+  p.NB = p.full ? 128 : outproj_nb(n_nodes);
   p.rows_pad = (n_nodes + p.NB - 1) / p.NB * p.NB;
-  // row blocks of 16 or 128 rows, one more per sequence for what its last block leaves empty
+  // row blocks, one more per sequence for what its last block leaves empty
   p.tc = v.kv_bits != 0 && max_nodes * v.group_q >= kTcFrom;
-  p.workers = p.tc ? num_sms() : tree_workers(v.kv_bits);
-  p.rb = p.tc ? kTcRows : 16;
+  // the fewest 8-row tiles that hold the rows, up to three (registers; bf16: two, and as many blocks as it takes)
+  const int rows = max_nodes * v.group_q;
+  p.nt = rows <= 8 ? 1 : rows <= 16 || v.kv_bits == 0 ? 2 : 3;
+  p.workers = p.tc ? num_sms()
+              : v.kv_bits == 0 ? mma_workers<0, 1>()
+              : p.nt == 1 ? mma_workers<8, 1>() : p.nt == 2 ? mma_workers<8, 2>() : mma_workers<8, 3>();
+  p.rb = p.tc ? kTcRows : 8 * p.nt;
   const size_t items = (size_t)v.Hkv * std::min((size_t)batch * ((max_nodes * v.group_q + p.rb - 1) / p.rb),
                                                 (size_t)batch + (size_t)n_nodes * v.group_q / p.rb);
   const size_t parts = items + p.workers;
@@ -1279,22 +1342,32 @@ TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes)
   p.pl = take(parts * p.rb * 4);
   p.pY = take(parts * p.rb * 512);
   p.y = take((size_t)p.rows_pad / p.NB * (L->Kp / 64) * p.NB * 128);
-  p.part = take(outproj_part_bytes(L, n_nodes));
+  p.part = take(p.full ? 0 : outproj_part_bytes(L, n_nodes));
   p.total = o;
   return p;
 }
 
+template <int BITS, int NT>
+cudaError_t launch_mma(const TreeMma& a, cudaStream_t s) {
+  const size_t smem = (size_t)kTreeWarps * MmaFmt<BITS, NT>::NS * PageFmt<BITS>::STAGE;
+  const cudaError_t e = set_smem_limit((const void*)k_tree_mma<BITS, NT>, smem);
+  if (e != cudaSuccess) return e;
+  k_tree_mma<BITS, NT><<<a.workers / kTreeWarps, 32 * kTreeWarps, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <int BITS>
 cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cudaStream_t s) {
-  using F = PageFmt<BITS>;
   const LayerView& v = L->view;
   const dim3 pgrid(a.t.n_nodes + 1, (v.H + kTreeWarps - 1) / kTreeWarps);
-  if (BITS == 4 && !p.tc)
-    k_tree_prep<BITS, 1><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
-  else if (BITS == 4)
-    k_tree_prep<BITS, 2><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
-  else
+  if constexpr (BITS == 4) {
+    if (p.tc)
+      k_tree_prep<BITS, 2><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
+    else
+      k_tree_prep<BITS, 1><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
+  } else {
     k_tree_prep<BITS, 0><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (BITS != 0 && p.tc) {
@@ -1303,10 +1376,9 @@ cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cu
     k_tree_tc<B><<<a.workers, kTcThreads, TcFmt<B>::SMEM, s>>>(a);
     return cudaGetLastError();
   }
-  const size_t smem = (size_t)kTreeWarps * F::NS * F::STAGE;
-  if ((e = set_smem_limit((const void*)k_tree_mma<BITS>, smem)) != cudaSuccess) return e;
-  k_tree_mma<BITS><<<a.workers / kTreeWarps, 32 * kTreeWarps, smem, s>>>(a);
-  return cudaGetLastError();
+  if (p.nt == 1) return launch_mma<BITS, 1>(a, s);
+  if (p.nt == 2 || BITS == 0) return launch_mma<BITS, 2>(a, s);
+  return launch_mma<BITS == 0 ? 8 : BITS, 3>(a, s);
 }
 
 }  // namespace
@@ -1340,9 +1412,12 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
   cudaError_t e = v.kv_bits == 8 ? launch_bits<8>(L, a, p, s) : v.kv_bits == 4 ? launch_bits<4>(L, a, p, s)
                                                                                : launch_bits<0>(L, a, p, s);
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)p.rows_pad * v.H;
-  k_tree_combine<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(a, p.rows_pad, p.NB, L->Kp / 64);
+  // a warp per head while that fills the SMs at most twice; else a row's heads share their row's lookups
+  const int hpw = (long long)p.rows_pad * v.H <= 128LL * num_sms() ? 1 : 8;
+  const long long warps = (long long)p.rows_pad * ((v.H + hpw - 1) / hpw);
+  k_tree_combine<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(a, p.rows_pad, p.NB, L->Kp / 64, hpw);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.full) return launch_out_full(L, a.w.y, t.n_nodes, t.out, t.lens ? nullptr : t.node_off + t.batch, s);
   return launch_outproj_tc(L, a.w.y, t.n_nodes, t.out, (float*)a.w.part, s, t.lens ? nullptr : t.node_off + t.batch);
 }
 
