@@ -11,6 +11,8 @@
 // (D/128) x (K/64) k-steps evenly (stream-K); a CTA whose range crosses an
 // output tile boundary flushes its accumulator there.  Partial sums go to the
 // workspace and a small kernel adds them in a fixed order.
+#include <type_traits>
+
 #include "tc_common.cuh"
 
 namespace starkv {
@@ -69,9 +71,17 @@ __global__ void __launch_bounds__(kOutThreads, 1) k_outproj_tc(OutArgs a) {
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_base;
+  tc::grid_launch_next();
 
   if (warp == 0) {
     if (lane == 0) {
+      // M does not depend on the kernels before: the first stages' tiles are on their way while those still run
+      const int ahead = (int)min((long long)a.stages, u1 - u0);
+      for (int i = 0; i < ahead; ++i) {
+        tc::mbar_expect_tx(&full[i], a_bytes + b_bytes);
+        tc::bulk_g2s(A_s + (size_t)i * a_bytes, a.M + ((size_t)u0 + i) * a_bytes, a_bytes, &full[i]);
+      }
+      tc::grid_wait_prev();
       // unit u = (output tile u / KT, k-tile u % KT); M tiles are stored in unit order
       int i = 0, s = 0;
       uint32_t ph = 0;
@@ -80,12 +90,14 @@ __global__ void __launch_bounds__(kOutThreads, 1) k_outproj_tc(OutArgs a) {
       const uint8_t* ybase = a.y + (size_t)nt * a.KTy * b_bytes;
       int dt = (int)(u0 / a.KT);
       for (long long u = u0; u < u1; ++u, ++i) {
-        if (!tc::mbar_wait(&empty[s], ph ^ 1u, a.status)) {
-          abort_flag = 1;
-          break;
+        if (i >= ahead) {
+          if (!tc::mbar_wait(&empty[s], ph ^ 1u, a.status)) {
+            abort_flag = 1;
+            break;
+          }
+          tc::mbar_expect_tx(&full[s], a_bytes + b_bytes);
+          tc::bulk_g2s(A_s + (size_t)s * a_bytes, msrc, a_bytes, &full[s]);
         }
-        tc::mbar_expect_tx(&full[s], a_bytes + b_bytes);
-        tc::bulk_g2s(A_s + (size_t)s * a_bytes, msrc, a_bytes, &full[s]);
         tc::bulk_g2s(B_s + (size_t)s * b_bytes, ybase + (size_t)(dt * a.y_step + kt) * b_bytes, b_bytes, &full[s]);
         msrc += a_bytes;
         if (++kt == a.KT) {
@@ -146,6 +158,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) k_outproj_tc(OutArgs a) {
     }
   } else {
     // epilogue: warps 2..5 cover TMEM lane quarters (warp % 4)
+    tc::grid_wait_prev();   // the partial sums may still be read by the kernel before
     const int q = warp & 3;
     const int n_local = q * 32 + lane;
     int seg = 0;
@@ -181,15 +194,16 @@ __global__ void __launch_bounds__(kOutThreads, 1) k_outproj_tc(OutArgs a) {
   if (warp == 1) tc::tmem_dealloc(tmem, a.tmem_cols);
 }
 
-// out[row][n] = sum over the CTAs whose k-range touched output tile n / 128.  A block takes `per` <= kReduceRows rows: one
-// for few rows (as many blocks as there are), four for many.
-constexpr int kReduceRows = 4;
-template <typename TO>
+// out[row][n] = sum over the CTAs whose k-range touched output tile n / 128.  A block takes PER rows: one for
+// few rows (as many blocks as there are), four for many.
+template <typename TO, int PER>
 __global__ void k_outproj_reduce(const float* __restrict__ part, int G, int KT, int DT, int slots, int NB, int rows,
-                                 int D, const int32_t* __restrict__ n_rows, int per, TO* __restrict__ out) {
+                                 int D, const int32_t* __restrict__ n_rows, TO* __restrict__ out) {
   __shared__ long long seg_off[512];
-  // kReduceRows rows of one row tile (NB is a multiple of 16): their segments lie at the same places, one row apart
-  const int dt = blockIdx.x, row = blockIdx.y * per;
+  // PER rows of one row tile (NB is a multiple of 16): their segments lie at the same places, one row apart
+  const int dt = blockIdx.x, row = blockIdx.y * PER;
+  tc::grid_launch_next();
+  tc::grid_wait_prev();
   if (n_rows) rows = min(rows, *n_rows);
   if (row >= rows) return;
   const int nt = row / NB, b = row % NB;
@@ -215,19 +229,19 @@ __global__ void k_outproj_reduce(const float* __restrict__ part, int G, int KT, 
   for (int n = threadIdx.x; n < 128; n += blockDim.x) {
     const int d = dt * 128 + n;
     if (d >= D) continue;
-    float acc[kReduceRows];
+    float acc[PER];
 #pragma unroll
-    for (int i = 0; i < kReduceRows; ++i) acc[i] = 0.f;
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
     for (int k = 0; k < nc; ++k) {
       const long long o = seg_off[k];
       if (o < 0) continue;
 #pragma unroll
-      for (int i = 0; i < kReduceRows; ++i)
-        if (i < per && row + i < rows) acc[i] += part[o + n + i * 128];
+      for (int i = 0; i < PER; ++i)
+        if (row + i < rows) acc[i] += part[o + n + i * 128];
     }
 #pragma unroll
-    for (int i = 0; i < kReduceRows; ++i)
-      if (i < per && row + i < rows) out[(size_t)(row + i) * D + d] = (TO)acc[i];
+    for (int i = 0; i < PER; ++i)
+      if (row + i < rows) out[(size_t)(row + i) * D + d] = (TO)acc[i];
   }
 }
 
@@ -274,7 +288,7 @@ size_t outproj_part_bytes(const starkv_layer* L, int rows) {
 
 cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, const void* y_tiles, int rows,
                            void* out, bool out_f32, float* part, uint32_t* status, cudaStream_t s, int y_group,
-                           const int32_t* n_rows) {
+                           const int32_t* n_rows, bool early) {
   const OutGeom g = gemm_geom(n_out, K);
   const int NB = outproj_nb(rows);
   const int ntiles = (rows + NB - 1) / NB;
@@ -300,21 +314,21 @@ cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, con
     OutArgs at = a;
     at.y = a.y + (size_t)t * a.KTy * NB * 128;
     at.part = part + (size_t)t * g.G * g.slots * NB * 128;
-    k_outproj_tc<<<dim3(g.G, 1), kOutThreads, smem, s>>>(at);
+    if ((e = launch_k(k_outproj_tc, dim3(g.G, 1), kOutThreads, smem, s, early, at)) != cudaSuccess) return e;
   }
-  const int per = rows > 32 ? kReduceRows : 1;
-  const dim3 rgrid(g.DT, (rows + per - 1) / per);
-  if (out_f32)
-    k_outproj_reduce<float><<<rgrid, 128, 0, s>>>(part, g.G, g.KT, g.DT, g.slots, NB, rows, n_valid, n_rows, per,
-                                                  (float*)out);
-  else
-    k_outproj_reduce<__nv_bfloat16><<<rgrid, 128, 0, s>>>(part, g.G, g.KT, g.DT, g.slots, NB, rows, n_valid, n_rows, per,
-                                                          (__nv_bfloat16*)out);
-  return cudaGetLastError();
+  auto reduce = [&](auto* o, auto per) {
+    constexpr int PER = decltype(per)::value;
+    return launch_k(k_outproj_reduce<std::remove_pointer_t<decltype(o)>, PER>, dim3(g.DT, (rows + PER - 1) / PER), 128, 0,
+                    s, early, (const float*)part, g.G, g.KT, g.DT, g.slots, NB, rows, n_valid, n_rows, o);
+  };
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
+  if (out_f32) return rows > 32 ? reduce((float*)out, Four{}) : reduce((float*)out, One{});
+  return rows > 32 ? reduce((__nv_bfloat16*)out, Four{}) : reduce((__nv_bfloat16*)out, One{});
 }
 
 cudaError_t launch_outproj_tc(const starkv_layer* L, const void* y_tiles, int rows, void* out, float* part,
-                              cudaStream_t s, const int32_t* n_rows) {
+                              cudaStream_t s, const int32_t* n_rows, bool early) {
   if (L->unfused) {
     const LayerView& v = L->view;
     uint8_t* w = (uint8_t*)part;
@@ -332,7 +346,7 @@ cudaError_t launch_outproj_tc(const starkv_layer* L, const void* y_tiles, int ro
                           n_rows);
   }
   return launch_gemm_tc((const uint8_t*)L->M_T, L->Dp, L->Kp, L->view.D, y_tiles, rows, out,
-                        L->view.dtype == STARKV_F32, part, L->status, s, 0, n_rows);
+                        L->view.dtype == STARKV_F32, part, L->status, s, 0, n_rows, early);
 }
 
 __device__ __forceinline__ float ld_any(const __nv_bfloat16* p, size_t i) { return __bfloat162float(p[i]); }

@@ -330,8 +330,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_full(GemmArgs a) {
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_base;
+  tc::grid_launch_next();
   if (warp == 0) {
     if (lane == 0) {
+      tc::grid_wait_prev();
       int k = 0;
       for (; k < a.KT; ++k) {
         const int s = k % a.stages;
@@ -419,6 +421,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_full(GemmArgs a) {
         }
       }
     }
+    if constexpr (EPI == EPI_OUT_BF16 || EPI == EPI_OUT_F32) tc::grid_wait_prev();
     const int rows = (EPI == EPI_OUT_BF16 || EPI == EPI_OUT_F32) && a.n_rows ? min(a.rows, *a.n_rows) : a.rows;
     for (int c0 = 0; c0 < (EPI == EPI_KROPE ? 0 : 128); c0 += 16) {
       float x[16];
@@ -951,7 +954,7 @@ cudaError_t launch_prefill_flash(const starkv_layer* L, const uint8_t* pool, lon
 }
 
 cudaError_t launch_out_full(const starkv_layer* L, const void* yt, int rows, void* out, const int32_t* n_rows,
-                            cudaStream_t s) {
+                            cudaStream_t s, bool early) {
   const LayerView& v = L->view;
   cudaError_t e;
   const int n_qt = (rows + kT - 1) / kT;
@@ -961,7 +964,10 @@ cudaError_t launch_out_full(const starkv_layer* L, const void* yt, int rows, voi
   go.B = (const uint8_t*)yt;
   go.b_step_x = (long long)(v.H * 128 / 64) * kAtomB;
   go.KT = v.H * 128 / 64;
-  go.stages = std::min(3, go.KT);
+  // Two stages when three blocks per SM then hold every tile at once and two (of three stages) do not: 320 tiles took
+  // 74 us in two waves.
+  const long long tiles = (long long)n_qt * ((v.D + 127) / 128);
+  go.stages = std::min(tiles > 2LL * num_sms() && tiles <= 3LL * num_sms() ? 2 : 3, go.KT);
   go.out = out;
   go.rows = rows;
   go.n_rows = n_rows;
@@ -973,10 +979,8 @@ cudaError_t launch_out_full(const starkv_layer* L, const void* yt, int rows, voi
   if ((e = set_smem_limit(gk, smem)) != cudaSuccess) return e;
   const dim3 grid(n_qt, (v.D + 127) / 128);
   if (v.dtype == STARKV_F32)
-    k_gemm_full<EPI_OUT_F32><<<grid, kGemmThreads, smem, s>>>(go);
-  else
-    k_gemm_full<EPI_OUT_BF16><<<grid, kGemmThreads, smem, s>>>(go);
-  return cudaGetLastError();
+    return launch_k(k_gemm_full<EPI_OUT_F32>, grid, kGemmThreads, smem, s, early, go);
+  return launch_k(k_gemm_full<EPI_OUT_BF16>, grid, kGemmThreads, smem, s, early, go);
 }
 
 }  // namespace starkv

@@ -61,6 +61,7 @@ struct TreeWs {
   long long* unit_off;   // [batch + 1] units before a sequence
   long long* item_off;   // [batch + 1] row blocks before a sequence
   void* q;               // [n_nodes][H][128] fp16 in the kernels' channel order; bf16 layers: the high, then the low parts
+  int* row_b;            // [n_nodes] sequence of a row, -1: none
   float *pm, *pl;        // [partials][rb]
   float* pY;             // [partials][rb][128]
   void* y;               // output tiles
@@ -165,6 +166,11 @@ __global__ void __launch_bounds__(128) k_tree_prep(TreeMma a) {
   }
   const int row = blockIdx.x, h = blockIdx.y * kTreeWarps + warp;
   if (h >= v.H) return;
+  if (h == 0) {
+    int b = t.lens ? row : -1;
+    if (!t.lens && row >= t.node_off[0] && row < t.node_off[t.batch]) b = warp_find(t.node_off, t.batch, row, lane);
+    if (lane == 0) a.w.row_b[row] = b;
+  }
   // lane: pairs p = 2 lane, 2 lane + 1 (channels p and p + 64)
   const __nv_bfloat162* q = reinterpret_cast<const __nv_bfloat162*>((const __nv_bfloat16*)t.q + ((size_t)row * v.H + h) * 128);
   const float2 lo = __bfloat1622float2(q[lane]), hi = __bfloat1622float2(q[32 + lane]);
@@ -328,6 +334,8 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
   uint8_t* ring = ring_all + (size_t)warp * NS * F::STAGE;
   const uint32_t ring_s = tc::smem_u32(ring);
   const int GQ = v.group_q;
+  tc::grid_wait_prev();
+  tc::grid_launch_next();
   const long long U = a.w.unit_off[t.batch];
   const int w = warp * gridDim.x + blockIdx.x;   // neighbouring runs on different SMs
   const long long We = workers_used(a, U);
@@ -877,6 +885,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
   const LayerView& v = a.v;
   const TreeArgs& t = a.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tc::grid_wait_prev();
+  tc::grid_launch_next();
   const long long U = a.w.unit_off[t.batch];
   const long long We = workers_used(a, U);
   const int w = blockIdx.x;
@@ -1250,11 +1260,9 @@ __global__ void __launch_bounds__(256) k_tree_combine(TreeMma a, int rows_pad, i
   const int parts = (v.H + hpw - 1) / hpw;
   if (id >= (long long)rows_pad * parts) return;
   const int row = (int)(id / parts), h0 = (int)(id % parts) * hpw;
-  int b = -1;
-  if (t.lens)
-    b = row < t.batch ? row : -1;
-  else if (row >= t.node_off[0] && row < t.node_off[t.batch])
-    b = warp_find(t.node_off, t.batch, row, lane);
+  // (what the query kernel wrote is complete: the attention kernel lets this one start only after its own wait for it)
+  tc::grid_launch_next();
+  const int b = row < t.n_nodes ? a.w.row_b[row] : -1;
   TreeSeq sq{0, 0, 0, 0};
   if (b >= 0) sq = seq_of(t, b, v.status, false);
   const bool live = sq.cnt > 0 && row >= sq.off && row - sq.off < sq.cnt && a.w.item_off[b + 1] > a.w.item_off[b];
@@ -1262,6 +1270,7 @@ __global__ void __launch_bounds__(256) k_tree_combine(TreeMma a, int rows_pad, i
   const long long U = a.w.unit_off[t.batch], We = workers_used(a, U);
   const long long u0 = live ? a.w.unit_off[b] : 0, i0 = live ? a.w.item_off[b] : 0;
   const int nt = row / NB, br = row % NB;
+  tc::grid_wait_prev();
   for (int h = h0; h < min(v.H, h0 + hpw); ++h) {
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
@@ -1277,8 +1286,8 @@ __global__ void __launch_bounds__(256) k_tree_combine(TreeMma a, int rows_pad, i
 #pragma unroll 4
       for (long long w = w0; w <= w1; ++w) {
         const long long p = (base + w) * a.rb + r;
-        const float f = ex2(a.w.pm[p] - m);
         const float4 x = *reinterpret_cast<const float4*>(a.w.pY + p * 128 + lane * 4);
+        const float f = ex2(a.w.pm[p] - m);
         l += f * a.w.pl[p];
         y.x += f * x.x;
         y.y += f * x.y;
@@ -1300,7 +1309,7 @@ template <int BITS, int NT>
 int mma_workers() { return MmaFmt<BITS, NT>::CTAS * kTreeWarps * num_sms(); }
 
 struct TreePlan {
-  size_t unit_off, item_off, q, pm, pl, pY, y, part, total;
+  size_t unit_off, item_off, q, row_b, pm, pl, pY, y, part, total;
   int NB, rows_pad;
   bool tc;               // k_tree_tc
   bool full;             // output product by 128 x 128 tiles, not stream-K
@@ -1338,6 +1347,7 @@ TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes)
   p.unit_off = take(8 * ((size_t)batch + 1));
   p.item_off = take(8 * ((size_t)batch + 1));
   p.q = take((size_t)n_nodes * v.H * 256 * (v.kv_bits == 0 ? 2 : 1));
+  p.row_b = take(4 * (size_t)n_nodes);
   p.pm = take(parts * p.rb * 4);
   p.pl = take(parts * p.rb * 4);
   p.pY = take(parts * p.rb * 512);
@@ -1352,8 +1362,7 @@ cudaError_t launch_mma(const TreeMma& a, cudaStream_t s) {
   const size_t smem = (size_t)kTreeWarps * MmaFmt<BITS, NT>::NS * PageFmt<BITS>::STAGE;
   const cudaError_t e = set_smem_limit((const void*)k_tree_mma<BITS, NT>, smem);
   if (e != cudaSuccess) return e;
-  k_tree_mma<BITS, NT><<<a.workers / kTreeWarps, 32 * kTreeWarps, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_k(k_tree_mma<BITS, NT>, a.workers / kTreeWarps, 32 * kTreeWarps, smem, s, true, a);
 }
 
 template <int BITS>
@@ -1373,8 +1382,7 @@ cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cu
   if (BITS != 0 && p.tc) {
     constexpr int B = BITS == 0 ? 8 : BITS;
     if ((e = set_smem_limit((const void*)k_tree_tc<B>, TcFmt<B>::SMEM)) != cudaSuccess) return e;
-    k_tree_tc<B><<<a.workers, kTcThreads, TcFmt<B>::SMEM, s>>>(a);
-    return cudaGetLastError();
+    return launch_k(k_tree_tc<B>, a.workers, kTcThreads, TcFmt<B>::SMEM, s, true, a);
   }
   if (p.nt == 1) return launch_mma<BITS, 1>(a, s);
   if (p.nt == 2 || BITS == 0) return launch_mma<BITS, 2>(a, s);
@@ -1400,6 +1408,7 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
   a.w.unit_off = (long long*)(w + p.unit_off);
   a.w.item_off = (long long*)(w + p.item_off);
   a.w.q = w + p.q;
+  a.w.row_b = (int*)(w + p.row_b);
   a.w.pm = (float*)(w + p.pm);
   a.w.pl = (float*)(w + p.pl);
   a.w.pY = (float*)(w + p.pY);
@@ -1415,10 +1424,11 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
   // a warp per head while that fills the SMs at most twice; else a row's heads share their row's lookups
   const int hpw = (long long)p.rows_pad * v.H <= 128LL * num_sms() ? 1 : 8;
   const long long warps = (long long)p.rows_pad * ((v.H + hpw - 1) / hpw);
-  k_tree_combine<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(a, p.rows_pad, p.NB, L->Kp / 64, hpw);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.full) return launch_out_full(L, a.w.y, t.n_nodes, t.out, t.lens ? nullptr : t.node_off + t.batch, s);
-  return launch_outproj_tc(L, a.w.y, t.n_nodes, t.out, (float*)a.w.part, s, t.lens ? nullptr : t.node_off + t.batch);
+  e = launch_k(k_tree_combine, (unsigned)((warps * 32 + 255) / 256), 256, 0, s, true, a, p.rows_pad, p.NB, L->Kp / 64, hpw);
+  if (e != cudaSuccess) return e;
+  const int32_t* n_rows = t.lens ? nullptr : t.node_off + t.batch;
+  if (p.full) return launch_out_full(L, a.w.y, t.n_nodes, t.out, n_rows, s, true);
+  return launch_outproj_tc(L, a.w.y, t.n_nodes, t.out, (float*)a.w.part, s, n_rows, true);
 }
 
 }  // namespace starkv

@@ -208,6 +208,23 @@ namespace starkv {
 
 void set_error(const std::string& msg);
 
+// Launch; with `early` the kernel may start while the one before it on the stream still runs (programmatic dependent
+// launch): it must call tc::grid_wait_prev() before it touches what that one writes or reads.
+template <typename... P, typename... A>
+cudaError_t launch_k(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool early, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // Kernel launchers (defined in the .cu files).
 cudaError_t launch_transpose_into(const void* src, int rows, int cols, int dtype, void* dst, int dst_row0,
                                   int dst_ld, cudaStream_t s);
@@ -292,7 +309,7 @@ cudaError_t launch_accept(const starkv_layer* L, uint8_t* pool, long long n_page
 // out = y W_o for many rows: y as fp16 tiles of 128 rows x 64 columns (head_dim 128).  n_rows (device, may be null): output
 // rows from *n_rows on are not written.
 cudaError_t launch_out_full(const starkv_layer* L, const void* yt, int rows, void* out, const int32_t* n_rows,
-                            cudaStream_t s);
+                            cudaStream_t s, bool early = false);
 // Tree attention (k_tree.cu).
 struct TreeArgs {
   const uint8_t* pool;
@@ -364,7 +381,7 @@ size_t outproj_part_bytes(const starkv_layer* L, int rows);
 // y's k-range [dt * K, dt * K + K) (y has n_out / 128 * K columns).
 cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, const void* y_tiles, int rows,
                            void* out, bool out_f32, float* part, uint32_t* status, cudaStream_t s, int y_group = 0,
-                           const int32_t* n_rows = nullptr);
+                           const int32_t* n_rows = nullptr, bool early = false);
 // Rows of a bf16 matrix as fp16 swizzled tiles of nb rows x 64 columns (nb = 0: the B-tile height for `rows`).
 cudaError_t launch_pack_rows_tiles(const void* x, int rows, int K, void* tiles, cudaStream_t s, int nb = 0);
 cudaError_t launch_pack_rows_tiles_f32(const float* x, int rows, int K, void* tiles, cudaStream_t s, int nb = 0);
@@ -379,8 +396,8 @@ cudaError_t launch_prefill_flash(const starkv_layer* L, const uint8_t* pool, lon
 // as tiles [Dp / 128][H d / 64] (built from the same inputs as M).
 cudaError_t launch_build_unfused(starkv_layer* L, const float* Bv_rot, const void* W_o, cudaStream_t s);
 size_t rows_tiles_bytes(int rows, int K);
-// n_rows (device, may be null): output rows from *n_rows on are not written.
+// n_rows (device, may be null): output rows from *n_rows on are not written.  early: see launch_k.
 cudaError_t launch_outproj_tc(const starkv_layer* L, const void* y_tiles, int rows, void* out, float* part,
-                              cudaStream_t s, const int32_t* n_rows = nullptr);
+                              cudaStream_t s, const int32_t* n_rows = nullptr, bool early = false);
 
 }  // namespace starkv

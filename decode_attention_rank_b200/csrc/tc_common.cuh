@@ -38,6 +38,12 @@ __device__ __host__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk)
   return (row >> 3) * 1024u + (row & 7u) * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
+// ---- programmatic dependent launch ------------------------------------------
+// (Both do nothing in a launch without the attribute.)  grid_launch_next lets the next kernel's blocks start as
+// resources come free; grid_wait_prev returns when the kernels before have completed and their writes are visible.
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait_prev() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- mbarrier -------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
