@@ -12,6 +12,8 @@
 // up to fp16; code = rne(x / scale) + 2^(b-1), the fp32 division.
 #include <float.h>
 
+#include <type_traits>
+
 #include "starkv_internal.cuh"
 
 namespace starkv {
@@ -81,36 +83,96 @@ __device__ __forceinline__ void angle(double turns, double* sn, double* cs) {
   sincospi(2.0 * (turns - rint(turns)), sn, cs);
 }
 
-// Norm and rotation of a row held as lo[V], hi[V] (channels V c .., half + V c ..) by a group of LPR lanes, in the
-// arithmetic F: float for what is rounded to 16 bits or compared in fp32, double for keys that a quantiser rounds
-// next, so that codes and scales do not depend on the order of a sum (packed pages equal the definition's bit for bit).
-template <typename F, int V, int LPR, typename CS>
-__device__ __forceinline__ void norm_rotate(float* lo, float* hi, const float* wl, const float* wh, float eps, int half,
-                                            CS cs, bool rope) {
-  F inv = 1;
-  if (wl) {
-    F s = 0;
+// Packed pairs of fp32 numbers (one register pair, one instruction for two products).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pk(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void upk(f32x2 x, float* a) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a[0]), "=f"(a[1]) : "l"(x)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A lane's factors for one kind of row: w cos and w sin of its channels' two halves (1 for no weights, no rotation), so that
+// a row costs two products an element and one by its norm.
+template <int V>
+struct Factors {
+  f32x2 lc[V / 2], hs[V / 2], hc[V / 2], ls[V / 2];   // w_lo cos, -w_hi sin, w_hi cos, w_lo sin
+};
+
+// 1 / sqrt(mean square + eps) of a row spread over LPR lanes.
+template <int V, int LPR>
+__device__ __forceinline__ float inv_rms(const float* lo, const float* hi, float eps, float rd) {
+  f32x2 a = pk(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < V; ++k) s += (F)lo[k] * (F)lo[k] + (F)hi[k] * (F)hi[k];
+  for (int k = 0; k < V; k += 2) {
+    const f32x2 x = pk(lo[k], lo[k + 1]), y = pk(hi[k], hi[k + 1]);
+    a = fma2(x, x, a);
+    a = fma2(y, y, a);
+  }
+  float s[2];
+  upk(a, s);
+  float t = s[0] + s[1];
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return rsqrtf(fmaf(t, rd, eps));
+}
+
+// lo, hi -> the normed and rotated row.
+template <int V>
+__device__ __forceinline__ void rotate_row(float* lo, float* hi, const Factors<V>& f, float inv) {
+  const f32x2 i2 = pk(inv, inv);
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) {
+    const f32x2 x = pk(lo[2 * k], lo[2 * k + 1]), y = pk(hi[2 * k], hi[2 * k + 1]);
+    upk(mul2(fma2(x, f.lc[k], mul2(y, f.hs[k])), i2), lo + 2 * k);
+    upk(mul2(fma2(y, f.hc[k], mul2(x, f.ls[k])), i2), hi + 2 * k);
+  }
+}
+
+// The same in 64 bits, for keys that a quantiser rounds next, so that codes and scales do not depend on the order of a sum
+// (packed pages equal the definition's bit for bit).  EXACT: x * w is exact in fp32 (bf16 rows and weights).
+template <int V, int LPR, bool EXACT>
+__device__ __forceinline__ void norm_rotate64(float* lo, float* hi, const float* wl, const float* wh, bool norm, double eps,
+                                              int d, const double2* cs, bool rope) {
+  double inv = 1;
+  if (norm) {
+    double s = 0;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (EXACT) {   // squares of bf16 numbers are exact in fp32
+        s += (double)(lo[k] * lo[k]);
+        s += (double)(hi[k] * hi[k]);
+      } else {
+        s += (double)lo[k] * (double)lo[k];
+        s += (double)hi[k] * (double)hi[k];
+      }
+    }
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    inv = F(1) / sqrt(s / F(2 * half) + (F)eps);
+    inv = rsqrt(s / (double)d + eps);
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    F x = lo[k], y = hi[k];
-    if (wl) {
-      x *= inv * (F)wl[k];
-      y *= inv * (F)wh[k];
-    }
+    double x = EXACT ? (double)(lo[k] * wl[k]) : (double)lo[k] * (double)wl[k];
+    double y = EXACT ? (double)(hi[k] * wh[k]) : (double)hi[k] * (double)wh[k];
     if (rope) {
-      const auto t = cs(k);
-      const F z = x * t.x - y * t.y;
+      const double2 t = cs[k];
+      const double z = x * t.x - y * t.y;
       y = y * t.x + x * t.y;
       x = z;
     }
-    lo[k] = (float)x;
-    hi[k] = (float)y;
+    lo[k] = (float)(x * inv);
+    hi[k] = (float)(y * inv);
   }
 }
 
@@ -136,21 +198,31 @@ __device__ __forceinline__ void quant_store(const float* x, uint8_t* blk, int sc
   const __half s16 = __float2half_ru(s32);
   const float sf = __half2float(s16);
   // code = rne(x / s): the product with 1 / s is within 2^-21 of the quotient's size (<= 127 and a rounding), so only a
-  // product that close to a border needs the division itself
+  // product that close to a border needs the division itself.  Adding 1.5 * 2^23 (and the even offset 2^(b-1)) rounds to an integer, to even
+  // at ties, and leaves it in the low bits; |x| <= amax keeps it inside the code's range.
   const float rs = sf != 0.f ? __fdiv_rn(1.f, sf) : 0.f;
+  constexpr float magic = 12582912.f + (float)(QM + 1);
   uint32_t u[V];
+  float near = 0.f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    float y = x[k] * rs;
-    if (fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f && sf != 0.f) y = __fdiv_rn(x[k], sf);
-    const int q = sf != 0.f ? min(max(__float2int_rn(y), -QM), QM) : 0;
-    u[k] = (uint32_t)(q + QM + 1);
+    const float y = x[k] * rs, z = y + magic;
+    near = fmaxf(near, fabsf(y - (z - magic)));
+    u[k] = __float_as_uint(z);
+  }
+  if (!fits) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) u[k] = QM + 1;
+  } else if (near > 0.4999f) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) u[k] = __float_as_uint(__fdiv_rn(x[k], sf) + magic);
   }
   uint8_t* dst = blk + scale_bytes + (size_t)group * GB + (size_t)slot * (32 * BITS / 8) + ch * BITS / 8;
   if constexpr (BITS == 8) {
     uint32_t w[V / 4];
 #pragma unroll
-    for (int k = 0; k < V / 4; ++k) w[k] = u[4 * k] | u[4 * k + 1] << 8 | u[4 * k + 2] << 16 | u[4 * k + 3] << 24;
+    for (int k = 0; k < V / 4; ++k)
+      w[k] = __byte_perm(__byte_perm(u[4 * k], u[4 * k + 1], 0x0040), __byte_perm(u[4 * k + 2], u[4 * k + 3], 0x0040), 0x5410);
     if constexpr (V == 8)
       *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else
@@ -158,7 +230,7 @@ __device__ __forceinline__ void quant_store(const float* x, uint8_t* blk, int sc
   } else {
     uint32_t w = 0;
 #pragma unroll
-    for (int k = 0; k < V; ++k) w |= u[k] << (4 * k);
+    for (int k = 0; k < V; ++k) w |= (u[k] & 15u) << (4 * k);
     if constexpr (V == 8)
       *reinterpret_cast<uint32_t*>(dst) = w;
     else
@@ -181,11 +253,11 @@ __device__ __forceinline__ void load_w(const float* w, int half, int c, float* w
   }
 }
 
-// A CTA takes a token and up to 8 * per of its row groups (32 / LPR heads each, LPR lanes to a row; first the queries'
-// groups, then the keys', then the values'); a warp takes every 8th of them, its next group's rows loaded before this
-// one's are worked on.  The token's cos / sin are made once per CTA; a lane's pairs are the same in every head, so
-// it keeps them, like its norm weights, in registers.  Bound: bytes.  Angles: the fraction of the turn in 64 bits, then
-// an fp32 sincos; in 64 bits throughout for keys that are quantised next (see norm_rotate).
+// A CTA takes a token and up to blockDim / 32 * per of its row groups (32 / LPR heads each, LPR lanes to a row; first the
+// queries' groups, then the keys', then the values'); its warps take them in turn, the next group's rows loaded before this
+// one's are worked on.  The token's cos / sin are made once per CTA; a lane's channels are the same in every head, so it
+// keeps its factors in registers.  Bound: bytes, then instructions (about 100 a group of rows).  Angles: the
+// fraction of the turn in 64 bits, then an fp32 sincos; in 64 bits throughout for keys that are quantised next.
 template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int per) {
   constexpr int V = Vec<T>::N, HALF = D / 2, LPR = HALF / V, RPW = 32 / LPR;
@@ -194,29 +266,8 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
   const LayerView& v = a.v;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x, nw = blockDim.x >> 5, b0 = blockIdx.y * nw * per, b1 = min(groups, b0 + nw * per);
-  const int g0 = b0 + warp;   // groups g0, g0 + nw, ...: the keys' and values' groups fall to different warps
   const int nq = a.q ? (v.H + RPW - 1) / RPW : 0, nk = a.k ? (v.Hkv + RPW - 1) / RPW : 0;
   const int c = lane % LPR, rr = lane / LPR;
-  auto source = [&](int g, bool& live) -> const T* {
-    const int kind = g < nq ? 0 : g < nq + nk ? 1 : 2;
-    const int h = (g - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * RPW + rr;
-    live = h < (kind == 0 ? v.H : v.Hkv);
-    const T* s = kind == 0 ? (const T*)a.q + (size_t)i * a.q_ld
-                           : kind == 1 ? (const T*)a.k + (size_t)i * a.k_ld : (const T*)a.vv + (size_t)i * a.v_ld;
-    return s + (size_t)h * D + c * V;
-  };
-  uint4 rl[V * sizeof(T) / 16], rh[V * sizeof(T) / 16];
-  auto fetch = [&](int g) {
-    bool live;
-    const T* s = source(g, live);
-    rl[0] = live ? *reinterpret_cast<const uint4*>(s) : make_uint4(0, 0, 0, 0);
-    rh[0] = live ? *reinterpret_cast<const uint4*>(s + HALF) : make_uint4(0, 0, 0, 0);
-  };
-  int slot = 0;
-  uint8_t* page = a.pool ? slot_page(a, i, &slot, lane == 0 && g0 == 0) : nullptr;
-  float wl[V], wh[V], cl[V], sl[V];
-  const float* w_now = nullptr;
-  if (g0 < b1) fetch(g0);
   if (a.rotate && b0 < nq + nk) {
     const double pos = (double)a.positions[i];
     for (int e = threadIdx.x; e < 2 * HALF; e += blockDim.x) {
@@ -231,68 +282,115 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
       }
     }
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < V; k += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(cs_c + c * V + k), y = *reinterpret_cast<const float4*>(cs_s + c * V + k);
-      cl[k] = x.x; cl[k + 1] = x.y; cl[k + 2] = x.z; cl[k + 3] = x.w;
-      sl[k] = y.x; sl[k + 1] = y.y; sl[k + 2] = y.z; sl[k + 3] = y.w;
-    }
   }
-  for (int g = g0; g < b1; g += nw) {
-    const int kind = g < nq ? 0 : g < nq + nk ? 1 : 2;
-    const int h = (g - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * RPW + rr;
-    const bool live = h < (kind == 0 ? v.H : v.Hkv);
-    float lo[V], hi[V];
-    Vec<T>::load(reinterpret_cast<const T*>(rl), lo);
-    Vec<T>::load(reinterpret_cast<const T*>(rh), hi);
-    if (g + nw < b1) fetch(g + nw);
-    if (kind != 2) {
-      const float* w = kind == 0 ? v.q_norm : v.k_norm;
-      if (w && w != w_now) load_w<V>(w, HALF, c, wl, wh);
-      w_now = w;
-      if (BITS && kind == 1)
-        norm_rotate<double, V, LPR>(lo, hi, w ? wl : nullptr, wh, v.norm_eps, HALF,
-                                    [&](int k) { return cs_d[c * V + k]; }, a.rotate);
-      else
-        norm_rotate<float, V, LPR>(lo, hi, w ? wl : nullptr, wh, v.norm_eps, HALF,
-                                   [&](int k) { return make_float2(cl[k], sl[k]); }, a.rotate);
-    }
-    if (kind == 0 || a.pool == nullptr) {
-      if (live) {
-        T* o = (kind == 0 ? (T*)a.q_out + (size_t)i * a.q_out_ld : (T*)a.k_out + (size_t)i * a.k_out_ld) + (size_t)h * D;
-        Vec<T>::store(o + c * V, lo);
-        Vec<T>::store(o + HALF + c * V, hi);
-      }
-      continue;
-    }
-    // block of KV head h's keys, or of all values, as the page lays them out
-    if constexpr (BITS != 0) {
-      constexpr int KB = D / 32 * (32 + 64 * BITS);
-      uint8_t* blk = page ? page + (size_t)(kind == 2 ? v.Hkv : h) * KB : nullptr;
-      const int sb = kind == 2 ? v.Hkv * D : D;   // bytes of the block's scales: one per 32 channels and slot, 2 bytes
-      const int gr = kind == 2 ? h * (D / 32) : 0, ch = c * V;
-      quant_store<BITS, V>(lo, blk, sb, gr + ch / 32, ch % 32, slot, live && page, v.status);
-      quant_store<BITS, V>(hi, blk, sb, gr + (HALF + ch) / 32, (HALF + ch) % 32, slot, live && page, v.status);
-    } else if (live && page) {
-      const size_t row = kind == 2 ? ((size_t)v.Hkv * kPage + (size_t)slot * v.Hkv + h) * D
-                                   : ((size_t)h * kPage + slot) * D;
-      if (v.es == 4) {
-        float* d = reinterpret_cast<float*>(page) + row + c * V;
+  int slot = 0;
+  uint8_t* page = a.pool ? slot_page(a, i, &slot, threadIdx.x == 0 && b0 == 0) : nullptr;
+  // this warp's groups of one kind: rows of `heads` heads at src (null: nothing of the kind)
+  auto run = [&](auto kind_c, int first, int count, int heads, const T* src, const float* w, T* out) {
+    constexpr int KIND = decltype(kind_c)::value;
+    constexpr bool WIDE = KIND == 1 && BITS != 0;
+    // the first group of this kind that is this warp's
+    int g = b0 + warp;
+    if (g < first) g += (first - g + nw - 1) / nw * nw;
+    const int end = min(b1, first + count);
+    if (g >= end) return;
+    src += c * V;
+    uint4 rl, rh;
+    auto fetch = [&](int gg) {
+      const int h = (gg - first) * RPW + rr;
+      const uint4* s = reinterpret_cast<const uint4*>(src + (size_t)h * D);
+      rl = h < heads ? s[0] : make_uint4(0, 0, 0, 0);
+      rh = h < heads ? s[HALF * sizeof(T) / 16] : make_uint4(0, 0, 0, 0);
+    };
+    fetch(g);
+    Factors<V> f;
+    float wl[V], wh[V];
+    if constexpr (KIND != 2) {
 #pragma unroll
-        for (int k = 0; k < V; k += 4) {
-          Vec<float>::store(d + k, lo + k);
-          Vec<float>::store(d + HALF + k, hi + k);
+      for (int k = 0; k < V; ++k) wl[k] = wh[k] = 1.f;
+      if (w) load_w<V>(w, HALF, c, wl, wh);
+      if constexpr (!WIDE) {
+        float cl[V], sl[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          cl[k] = a.rotate ? cs_c[c * V + k] : 1.f;
+          sl[k] = a.rotate ? cs_s[c * V + k] : 0.f;
         }
-      } else {
-        __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(page) + row + c * V;
 #pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          *reinterpret_cast<__nv_bfloat162*>(d + k) = __floats2bfloat162_rn(lo[k], lo[k + 1]);
-          *reinterpret_cast<__nv_bfloat162*>(d + HALF + k) = __floats2bfloat162_rn(hi[k], hi[k + 1]);
+        for (int k = 0; k < V / 2; ++k) {
+          const f32x2 cc = pk(cl[2 * k], cl[2 * k + 1]), ss = pk(sl[2 * k], sl[2 * k + 1]), ns = pk(-sl[2 * k], -sl[2 * k + 1]);
+          const f32x2 a2 = pk(wl[2 * k], wl[2 * k + 1]), b2 = pk(wh[2 * k], wh[2 * k + 1]);
+          f.lc[k] = mul2(a2, cc);
+          f.hs[k] = mul2(b2, ns);
+          f.hc[k] = mul2(b2, cc);
+          f.ls[k] = mul2(a2, ss);
         }
       }
     }
-  }
+    for (; g < end; g += nw) {
+      const int h = (g - first) * RPW + rr;
+      const bool live = h < heads;
+      float lo[V], hi[V];
+      Vec<T>::load(reinterpret_cast<const T*>(&rl), lo);
+      Vec<T>::load(reinterpret_cast<const T*>(&rh), hi);
+      if (g + nw < end) fetch(g + nw);
+      if constexpr (WIDE) {
+        norm_rotate64<V, LPR, sizeof(T) == 2>(lo, hi, wl, wh, w != nullptr, (double)v.norm_eps, D, cs_d + c * V, a.rotate);
+      } else if constexpr (KIND != 2) {
+        const float inv = w ? inv_rms<V, LPR>(lo, hi, v.norm_eps, 1.f / D) : 1.f;
+        rotate_row<V>(lo, hi, f, inv);
+      }
+      if (KIND == 0 || a.pool == nullptr) {
+        if (live) {
+          T* o = out + (size_t)h * D + c * V;
+          Vec<T>::store(o, lo);
+          Vec<T>::store(o + HALF, hi);
+        }
+        continue;
+      }
+      // block of KV head h's keys, or of all values, as the page lays them out
+      if constexpr (BITS != 0) {
+        constexpr int KB = D / 32 * (32 + 64 * BITS);
+        uint8_t* blk = page ? page + (size_t)(KIND == 2 ? v.Hkv : h) * KB : nullptr;
+        const int sb = KIND == 2 ? v.Hkv * D : D;   // bytes of the block's scales: one per 32 channels and slot, 2 bytes
+        const int gr = KIND == 2 ? h * (D / 32) : 0, ch = c * V;
+        quant_store<BITS, V>(lo, blk, sb, gr + ch / 32, ch % 32, slot, live && page, v.status);
+        quant_store<BITS, V>(hi, blk, sb, gr + (HALF + ch) / 32, (HALF + ch) % 32, slot, live && page, v.status);
+      } else if (live && page) {
+        const size_t row = KIND == 2 ? ((size_t)v.Hkv * kPage + (size_t)slot * v.Hkv + h) * D
+                                     : ((size_t)h * kPage + slot) * D;
+        if (v.es == 4) {
+          float* d = reinterpret_cast<float*>(page) + row + c * V;
+#pragma unroll
+          for (int k = 0; k < V; k += 4) {
+            Vec<float>::store(d + k, lo + k);
+            Vec<float>::store(d + HALF + k, hi + k);
+          }
+        } else {
+          __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(page) + row + c * V;
+          if constexpr (V == 8) {
+            Vec<__nv_bfloat16>::store(d, lo);
+            Vec<__nv_bfloat16>::store(d + HALF, hi);
+          } else {
+#pragma unroll
+            for (int k = 0; k < V; k += 2) {
+              *reinterpret_cast<__nv_bfloat162*>(d + k) = __floats2bfloat162_rn(lo[k], lo[k + 1]);
+              *reinterpret_cast<__nv_bfloat162*>(d + HALF + k) = __floats2bfloat162_rn(hi[k], hi[k + 1]);
+            }
+          }
+        }
+      }
+    }
+  };
+  if (a.q)
+    run(std::integral_constant<int, 0>{}, 0, nq, v.H, (const T*)a.q + (size_t)i * a.q_ld, v.q_norm,
+        (T*)a.q_out + (size_t)i * a.q_out_ld);
+  if (a.k)
+    run(std::integral_constant<int, 1>{}, nq, nk, v.Hkv, (const T*)a.k + (size_t)i * a.k_ld, v.k_norm,
+        a.pool ? nullptr : (T*)a.k_out + (size_t)i * a.k_out_ld);
+  if (a.vv)
+    run(std::integral_constant<int, 2>{}, nq + nk, groups - nq - nk, v.Hkv, (const T*)a.vv + (size_t)i * a.v_ld, nullptr,
+        nullptr);
 }
 
 // Any even head_dim up to 256, unquantised pages: one warp per row, a lane per pair.
@@ -362,10 +460,10 @@ cudaError_t launch_qkv_d(const KvArgs& a, cudaStream_t s) {
   constexpr int RPW = 32 / (D / 2 / Vec<T>::N), NW = kKvThreads / 32;
   const int gq = (a.v.H + RPW - 1) / RPW, gk = (a.v.Hkv + RPW - 1) / RPW;
   const int groups = (a.q ? gq : 0) + (a.k ? gk : 0) + (a.vv ? gk : 0);
-  // Many tokens: one CTA for a whole token.  Few: a row group per warp, the token over several CTAs, for latency.
+  // Many tokens: one CTA for a whole token, four warps (they share the angles and keep their factors over several groups).
+  // Few: a row group per warp, the token over several CTAs, for latency.
   const bool many = (long long)a.n * groups > 64LL * num_sms();
-  const int per = many ? (groups + NW - 1) / NW : 1;
-  const int nw = std::min(NW, (groups + per - 1) / per);
+  const int nw = std::min(many ? 4 : NW, groups), per = many ? (groups + nw - 1) / nw : 1;
   k_qkv<T, D, BITS><<<dim3((unsigned)a.n, (unsigned)((groups + nw * per - 1) / (nw * per))), 32 * nw, 0, s>>>(a, groups, per);
   return cudaGetLastError();
 }
