@@ -159,14 +159,14 @@ __device__ __forceinline__ void norm_rotate64(float* lo, float* hi, const float*
     }
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    inv = rsqrt(s / (double)d + eps);
+    inv = rsqrt(s * (1.0 / d) + eps);   // d is a power of two
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     double x = EXACT ? (double)(lo[k] * wl[k]) : (double)lo[k] * (double)wl[k];
     double y = EXACT ? (double)(hi[k] * wh[k]) : (double)hi[k] * (double)wh[k];
     if (rope) {
-      const double2 t = cs[k];
+      const double2 t = cs[k * LPR];
       const double z = x * t.x - y * t.y;
       y = y * t.x + x * t.y;
       x = z;
@@ -268,6 +268,22 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
   const int i = blockIdx.x, nw = blockDim.x >> 5, b0 = blockIdx.y * nw * per, b1 = min(groups, b0 + nw * per);
   const int nq = a.q ? (v.H + RPW - 1) / RPW : 0, nk = a.k ? (v.Hkv + RPW - 1) / RPW : 0;
   const int c = lane % LPR, rr = lane / LPR;
+  // the rows of this warp's next group, asked for ahead
+  uint4 rl, rh;
+  auto fetch = [&](int g) {
+    const int kind = g < nq ? 0 : g < nq + nk ? 1 : 2;
+    const int h = (g - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * RPW + rr;
+    const T* s = kind == 0 ? (const T*)a.q + (size_t)i * a.q_ld
+                           : kind == 1 ? (const T*)a.k + (size_t)i * a.k_ld : (const T*)a.vv + (size_t)i * a.v_ld;
+    const uint4* p = reinterpret_cast<const uint4*>(s + (size_t)h * D + c * V);
+    const bool live = h < (kind == 0 ? v.H : v.Hkv);
+    rl = live ? p[0] : make_uint4(0, 0, 0, 0);
+    rh = live ? p[HALF * sizeof(T) / 16] : make_uint4(0, 0, 0, 0);
+  };
+  int g = b0 + warp;
+  if (g < b1) fetch(g);
+  int slot = 0;
+  uint8_t* page = a.pool ? slot_page(a, i, &slot, threadIdx.x == 0 && b0 == 0) : nullptr;
   if (a.rotate && b0 < nq + nk) {
     const double pos = (double)a.positions[i];
     for (int e = threadIdx.x; e < 2 * HALF; e += blockDim.x) {
@@ -278,31 +294,17 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
       } else if (BITS && b1 > nq) {
         double sn, cs;
         angle(pos * a.turn[p], &sn, &cs);
-        cs_d[p] = make_double2(cs, sn);
+        cs_d[p % V * LPR + p / V] = make_double2(cs, sn);   // (lanes read neighbours: no bank conflicts)
       }
     }
     __syncthreads();
   }
-  int slot = 0;
-  uint8_t* page = a.pool ? slot_page(a, i, &slot, threadIdx.x == 0 && b0 == 0) : nullptr;
-  // this warp's groups of one kind: rows of `heads` heads at src (null: nothing of the kind)
-  auto run = [&](auto kind_c, int first, int count, int heads, const T* src, const float* w, T* out) {
+  // this warp's groups of one kind: rows of `heads` heads
+  auto run = [&](auto kind_c, int first, int count, int heads, const float* w, T* out) {
     constexpr int KIND = decltype(kind_c)::value;
     constexpr bool WIDE = KIND == 1 && BITS != 0;
-    // the first group of this kind that is this warp's
-    int g = b0 + warp;
-    if (g < first) g += (first - g + nw - 1) / nw * nw;
     const int end = min(b1, first + count);
     if (g >= end) return;
-    src += c * V;
-    uint4 rl, rh;
-    auto fetch = [&](int gg) {
-      const int h = (gg - first) * RPW + rr;
-      const uint4* s = reinterpret_cast<const uint4*>(src + (size_t)h * D);
-      rl = h < heads ? s[0] : make_uint4(0, 0, 0, 0);
-      rh = h < heads ? s[HALF * sizeof(T) / 16] : make_uint4(0, 0, 0, 0);
-    };
-    fetch(g);
     Factors<V> f;
     float wl[V], wh[V];
     if constexpr (KIND != 2) {
@@ -333,9 +335,9 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
       float lo[V], hi[V];
       Vec<T>::load(reinterpret_cast<const T*>(&rl), lo);
       Vec<T>::load(reinterpret_cast<const T*>(&rh), hi);
-      if (g + nw < end) fetch(g + nw);
+      if (g + nw < b1) fetch(g + nw);
       if constexpr (WIDE) {
-        norm_rotate64<V, LPR, sizeof(T) == 2>(lo, hi, wl, wh, w != nullptr, (double)v.norm_eps, D, cs_d + c * V, a.rotate);
+        norm_rotate64<V, LPR, sizeof(T) == 2>(lo, hi, wl, wh, w != nullptr, (double)v.norm_eps, D, cs_d + c, a.rotate);
       } else if constexpr (KIND != 2) {
         const float inv = w ? inv_rms<V, LPR>(lo, hi, v.norm_eps, 1.f / D) : 1.f;
         rotate_row<V>(lo, hi, f, inv);
@@ -383,14 +385,11 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
     }
   };
   if (a.q)
-    run(std::integral_constant<int, 0>{}, 0, nq, v.H, (const T*)a.q + (size_t)i * a.q_ld, v.q_norm,
-        (T*)a.q_out + (size_t)i * a.q_out_ld);
+    run(std::integral_constant<int, 0>{}, 0, nq, v.H, v.q_norm, (T*)a.q_out + (size_t)i * a.q_out_ld);
   if (a.k)
-    run(std::integral_constant<int, 1>{}, nq, nk, v.Hkv, (const T*)a.k + (size_t)i * a.k_ld, v.k_norm,
-        a.pool ? nullptr : (T*)a.k_out + (size_t)i * a.k_out_ld);
+    run(std::integral_constant<int, 1>{}, nq, nk, v.Hkv, v.k_norm, a.pool ? nullptr : (T*)a.k_out + (size_t)i * a.k_out_ld);
   if (a.vv)
-    run(std::integral_constant<int, 2>{}, nq + nk, groups - nq - nk, v.Hkv, (const T*)a.vv + (size_t)i * a.v_ld, nullptr,
-        nullptr);
+    run(std::integral_constant<int, 2>{}, nq + nk, groups - nq - nk, v.Hkv, nullptr, nullptr);
 }
 
 // Any even head_dim up to 256, unquantised pages: one warp per row, a lane per pair.
