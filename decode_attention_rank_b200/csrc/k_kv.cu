@@ -96,6 +96,11 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -500,67 +505,108 @@ __global__ void __launch_bounds__(32 * kReadWarps) k_read8(KvArgs a, int chunks_
   const long long i = (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
   if (i >= a.n) return;
   const int cph = CPH ? CPH : v.d / 8, d = CPH ? CPH * 8 : v.d;
-  const int chunks = 2 * v.Hkv * cph;
+  const int keys = v.Hkv * cph, chunks = 2 * keys;
   const int e0 = blockIdx.y * chunks_per_warp, e1 = min(chunks, e0 + chunks_per_warp);
   int slot = 0;
   const uint8_t* page = slot_page(a, (int)i, &slot, lane == 0 && e0 == 0);
   TO* row = out + (size_t)i * (chunks * 8);
-  // kReadUnroll chunks' bytes are asked for before the first is used
-  for (int eb = e0 + lane; eb < e1; eb += 32 * kReadUnroll) {
-    uint4 raw[kReadUnroll][BITS == 0 && sizeof(TO) == 4 ? 2 : 1];
-    __half sc[kReadUnroll];
+  constexpr int GB = kPage * 32 * (BITS ? BITS : 8) / 8;            // bytes of a group's codes
+  const int kb = BITS ? d / 32 * (32 + GB) : d * kPage * (int)sizeof(TO);   // bytes of a head's key block
+  // chunks eb .. of one side (keys, or values): chunk e's codes at c + steps * cstep, its scale at s + steps * sstep
+  auto run = [&](int eb, int end, const uint8_t* c, int cstep, const uint8_t* s, int sstep) {
+    // kReadUnroll chunks' bytes are asked for before the first is used
+    for (; eb < end; eb += 32 * kReadUnroll) {
+      uint4 raw[kReadUnroll][BITS == 0 && sizeof(TO) == 4 ? 2 : 1];
+      __half sc[kReadUnroll];
 #pragma unroll
-    for (int x = 0; x < kReadUnroll; ++x) {
-      const int e = eb + 32 * x;
-      raw[x][0] = make_uint4(0, 0, 0, 0);
-      if constexpr (BITS == 0 && sizeof(TO) == 4) raw[x][1] = raw[x][0];
-      sc[x] = __float2half_rn(0.f);
-      if (e >= e1 || !page) continue;
-      const int h = e / cph, j = (e % cph) * 8;   // heads Hkv .. 2 Hkv - 1: values
-      const bool val = h >= v.Hkv;
-      if constexpr (BITS == 0) {
-        const size_t o = val ? ((size_t)v.Hkv * kPage + (size_t)slot * v.Hkv + (h - v.Hkv)) * d + j
-                             : ((size_t)h * kPage + slot) * d + j;
-        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const TO*>(page) + o);
-        raw[x][0] = p[0];
-        if constexpr (sizeof(TO) == 4) raw[x][1] = p[1];
-      } else {
-        constexpr int GB = kPage * 32 * BITS / 8;
-        const int kb = d / 32 * (32 + GB);
-        const int g = (val ? (h - v.Hkv) * (d / 32) : 0) + j / 32;
-        const uint8_t* blk = page + (size_t)(val ? v.Hkv : h) * kb;
-        sc[x] = reinterpret_cast<const __half*>(blk)[g * kPage + slot];
-        const uint8_t* c = blk + (val ? v.Hkv * d : d) + (size_t)g * GB + (size_t)slot * (4 * BITS) + (j % 32) * BITS / 8;
-        if constexpr (BITS == 8) {
-          const uint2 u = *reinterpret_cast<const uint2*>(c);
-          raw[x][0].x = u.x;
-          raw[x][0].y = u.y;
+      for (int x = 0; x < kReadUnroll; ++x) {
+        raw[x][0] = make_uint4(0, 0, 0, 0);
+        if constexpr (BITS == 0 && sizeof(TO) == 4) raw[x][1] = raw[x][0];
+        sc[x] = __float2half_rn(0.f);
+        if (eb + 32 * x < end && page) {
+          if constexpr (BITS == 0) {
+            raw[x][0] = reinterpret_cast<const uint4*>(c)[0];
+            if constexpr (sizeof(TO) == 4) raw[x][1] = reinterpret_cast<const uint4*>(c)[1];
+          } else {
+            sc[x] = *reinterpret_cast<const __half*>(s);
+            if constexpr (BITS == 8) {
+              const uint2 u = *reinterpret_cast<const uint2*>(c);
+              raw[x][0].x = u.x;
+              raw[x][0].y = u.y;
+            } else {
+              raw[x][0].x = *reinterpret_cast<const uint32_t*>(c);
+            }
+          }
+        }
+        c += cstep;
+        s += sstep;
+      }
+#pragma unroll
+      for (int x = 0; x < kReadUnroll; ++x) {
+        if (eb + 32 * x >= end) break;
+        TO* o = row + (eb + 32 * x) * 8;
+        if constexpr (BITS == 0) {
+          reinterpret_cast<uint4*>(o)[0] = raw[x][0];
+          if constexpr (sizeof(TO) == 4) reinterpret_cast<uint4*>(o)[1] = raw[x][1];
         } else {
-          raw[x][0].x = *reinterpret_cast<const uint32_t*>(c);
+          float f[8];
+          const float sf = __half2float(sc[x]);
+          const f32x2 s2 = pk(sf, sf);
+          if constexpr (BITS == 8) {
+            // a code in the low byte of 2^23 is the number 2^23 + u (an integer conversion has a sixteenth of the rate)
+            const f32x2 off = pk(-8388736.f, -8388736.f);
+            auto code = [&](int k) {
+              return __uint_as_float(__byte_perm(k < 4 ? raw[x][0].x : raw[x][0].y, 0x4B000000u, 0x7440 + k % 4));
+            };
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) upk(mul2(add2(pk(code(k), code(k + 1)), off), s2), f + k);
+          } else {
+            // codes k, k + 4 under the exponent of 1024 (fp16), exact integers after one subtraction
+            const uint32_t w = raw[x][0].x, w8 = w >> 8;
+            const __half2 off = __floats2half2_rn(-1032.f, -1032.f), o16 = __floats2half2_rn(-72.f, -72.f),
+                          s16 = __floats2half2_rn(0.0625f, 0.0625f);
+            auto h = [](uint32_t y) { return *reinterpret_cast<const __half2*>(&y); };
+            const float2 a0 = __half22float2(__hadd2(h((w & 0x000F000Fu) | 0x64006400u), off));
+            const float2 a1 = __half22float2(__hfma2(h((w & 0x00F000F0u) | 0x64006400u), s16, o16));
+            const float2 a2 = __half22float2(__hadd2(h((w8 & 0x000F000Fu) | 0x64006400u), off));
+            const float2 a3 = __half22float2(__hfma2(h((w8 & 0x00F000F0u) | 0x64006400u), s16, o16));
+            upk(mul2(pk(a0.x, a1.x), s2), f);
+            upk(mul2(pk(a2.x, a3.x), s2), f + 2);
+            upk(mul2(pk(a0.y, a1.y), s2), f + 4);
+            upk(mul2(pk(a2.y, a3.y), s2), f + 6);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; k += Vec<TO>::N) Vec<TO>::store(o + k, f + k);
         }
       }
     }
-#pragma unroll
-    for (int x = 0; x < kReadUnroll; ++x) {
-      const int e = eb + 32 * x;
-      if (e >= e1) break;
-      TO* o = row + e * 8;
-      if constexpr (BITS == 0) {
-        reinterpret_cast<uint4*>(o)[0] = raw[x][0];
-        if constexpr (sizeof(TO) == 4) reinterpret_cast<uint4*>(o)[1] = raw[x][1];
-      } else {
-        float f[8];
-        const float s = __half2float(sc[x]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int u = BITS == 8 ? (int)(((k < 4 ? raw[x][0].x : raw[x][0].y) >> (8 * (k % 4))) & 255u) - 128
-                                  : (int)((raw[x][0].x >> (4 * k)) & 15u) - 8;
-          f[k] = (float)u * s;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; k += Vec<TO>::N) Vec<TO>::store(o + k, f + k);
-      }
+  };
+  // 32 chunks on: for keys 32 / cph heads, for values 8 groups
+  if (e0 < keys) {
+    const int e = e0 + lane;
+    if constexpr (CPH != 0) {   // (8, 16 or 32 chunks: they divide 32)
+      const int h = e / CPH, j = e % CPH;
+      const uint8_t* blk = page + (size_t)h * kb;
+      if constexpr (BITS != 0)
+        run(e, min(e1, keys), blk + d + (j >> 2) * GB + slot * (4 * BITS) + (j & 3) * BITS, 32 / CPH * kb,
+            blk + (j >> 2) * 32 + slot * 2, 32 / CPH * kb);
+      else
+        run(e, min(e1, keys), blk + (slot * d + j * 8) * sizeof(TO), 32 / CPH * kb, nullptr, 0);
+    } else {
+      // rows of any number of chunks: one step at a time
+      for (int x = e; x < min(e1, keys); x += 32)
+        run(x, min(x + 1, keys), page + (size_t)(x / cph) * kb + (size_t)slot * d * sizeof(TO) + (x % cph) * 8 * sizeof(TO), 0,
+            nullptr, 0);
     }
+  }
+  if (e1 > keys) {
+    const int e = max(e0, keys) + lane;
+    const int x = e - keys;
+    const uint8_t* blk = page + (size_t)v.Hkv * kb;
+    if constexpr (BITS != 0)
+      run(e, e1, blk + v.Hkv * d + (x >> 2) * GB + slot * (4 * BITS) + (x & 3) * BITS, 8 * GB, blk + (x >> 2) * 32 + slot * 2, 256);
+    else
+      run(e, e1, blk + ((size_t)slot * v.Hkv * d + x * 8) * sizeof(TO), 256 * (int)sizeof(TO), nullptr, 0);
   }
 }
 
@@ -815,12 +861,12 @@ void read_plain(const KvArgs& a, void* out, cudaStream_t s) {
   const dim3 grid((unsigned)rows, (unsigned)((chunks + per - 1) / per));
   if (a.v.d == 128)
     k_read8<TO, BITS, 16><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
-  else if (BITS == 0)
-    k_read8<TO, 0, 0><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
   else if (a.v.d == 64)
     k_read8<TO, BITS, 8><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
-  else
+  else if (a.v.d == 256)
     k_read8<TO, BITS, 32><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
+  else
+    k_read8<TO, 0, 0><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
 }
 
 }  // namespace

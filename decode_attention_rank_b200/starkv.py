@@ -121,12 +121,24 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+_torch_module = None
+
+
+def _torch():
+    """torch, imported at the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _rows(t, n: int, width: int, name: str, dtype, dense: bool = False):
     """Pointer and row stride of n rows of `width` elements ([n, width] or [n, heads, d]; rows may be strided)."""
     if t is None:
         return None, 0
     shape, stride = t.shape, t.stride()
-    last = shape[-1] if shape else 0
+    last = shape[-1] if len(shape) else 0
     if len(shape) == 3 and (shape[1] == 1 or stride[1] == last):
         last *= shape[1]
     elif len(shape) != 2:
@@ -135,16 +147,17 @@ def _rows(t, n: int, width: int, name: str, dtype, dense: bool = False):
         raise ValueError(f"{name} must be [{n}, {width}] with contiguous rows, got {list(shape)}, strides {list(stride)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must have the layer's dtype ({dtype}), got {t.dtype}")
-    if dense and n > 1 and stride[0] != width:
+    ld = stride[0] if n > 1 else width
+    if dense and ld != width:
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr(), stride[0] if n > 1 else width
+    return t.data_ptr(), ld
 
 
 def _ints(t, n: int, name: str):
     """Pointer of a contiguous int32 array of n elements."""
     if t is None:
         return None
-    if t.dtype is not _torch().int32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _torch_module.int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 array of {n} elements")
     return t.data_ptr()
 
@@ -157,15 +170,9 @@ def _table(page_table, batch: int = 0):
     return _ints(page_table, rows * cols, "page_table"), rows, cols
 
 
-def _torch():
-    import torch
-    return torch
-
-
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _torch().cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -316,8 +323,8 @@ class Layer:
 
     def cache_read(self, pool, n_pages: int, page_table, seq_idx, slots, out, stream=None) -> None:
         """Cached tokens as dense rows [n, latent_total]."""
-        n = seq_idx.numel()
-        op, _ = _rows(out, n, self.latent_total, "out", self._shape()[0], dense=True)
+        dt, n = self._shape()[0], seq_idx.numel()
+        op, _ = _rows(out, n, self.latent_total, "out", dt, dense=True)
         pt, seqs, mp = _table(page_table)
         _check(_lib.starkv_cache_read(self._h, _ptr(pool), n_pages, pt, seqs, mp, n, _ints(seq_idx, n, "seq_idx"),
                                       _ints(slots, n, "slots"), op, _stream(stream)), "starkv_cache_read")
@@ -347,6 +354,7 @@ class Layer:
     def tree_accept(self, pool, n_pages: int, page_table, hist, node_off, acc, n_acc, max_nodes: int,
                     stream=None) -> None:
         """Move the accepted nodes' slots to the front and clear the other nodes' slots."""
+        self._shape()
         batch, n = hist.numel(), acc.numel()
         pt, _, mp = _table(page_table, batch)
         _check(_lib.starkv_tree_accept(self._h, _ptr(pool), n_pages, pt, mp, batch, _ints(hist, batch, "hist"),
