@@ -52,7 +52,7 @@ struct PageFmt {
 // two parts), ring stages by shared memory.
 template <int BITS, int NT>
 struct MmaFmt {
-  static constexpr int CTAS = BITS == 0 ? 2 : NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int CTAS = BITS == 0 ? 2 : NT == 1 ? 4 : 2;
   static constexpr int NS = (int)(212 * 1024 / (CTAS * kTreeWarps) / PageFmt<BITS>::STAGE) < 8
                                 ? (int)(212 * 1024 / (CTAS * kTreeWarps) / PageFmt<BITS>::STAGE) : 8;
 };
@@ -703,14 +703,15 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
 //   warps 0 - 7   dequantisation: each owns one page of every tile, with its own ring of 16-byte asynchronous copies (one
 //                 copying warp with bulk copies of 128 to 2176 bytes took 2400 cycles a tile to issue them); a lane
 //                 takes a slot's group of 32 channels, a warp 8 slots x 4 groups, so that its 16-byte stores do not conflict
-//   warp 8        MMA issue: S(0), S(1), then O += P(k) V(k) and S(k + 2)
-//   warps 9 ..    softmax, 8 warps, one row per thread: four take the even tiles, four the odd ones, so that one set's
+//   warp 19       MMA issue: S(0), S(1), then O += P(k) V(k) and S(k + 2)
+//   warps 8 - 15  softmax, one row per thread: four take the even tiles, four the odd ones, so that one set's
 //                 exponentials run beside the other's loads and maxima.  The row's running maximum is handed from tile to
 //                 tile through shared memory as soon as it is known; rows past the block's are skipped by the warp.  P
 //                 overwrites S in TMEM; O is rescaled when the maximum grew by more than 2^8.
 // TMEM: S in two 128-column buffers, O in 256 .. 383, Q in 384 .. 447.  Units of work: tiles, dealt to the CTAs as above.
 constexpr int kTcDeq = 8, kTcSoft = 8;
-constexpr int kTcThreads = 32 * (1 + kTcDeq + kTcSoft);
+constexpr int kTcMma = 19;             // (the scheduler of lane quarter 3, whose rows are used least; warps 16 - 18 only wait)
+constexpr int kTcThreads = 32 * (kTcMma + 1);
 constexpr int kTcTile = 32768, kTcAtom = 16384;
 
 template <int BITS>
@@ -911,14 +912,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
     abort_flag = 0;
     tc::fence_mbar_init();
   }
-  if (warp == kTcDeq) tc::tmem_alloc(&tmem_base, 512);
+  if (warp == kTcMma) tc::tmem_alloc(&tmem_base, 512);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_base;
   constexpr uint32_t o_col = 256, q_col = 384;
 
-  if (warp == kTcDeq) {
+  if (warp == kTcMma) {
     // ------------------------------------------------ MMA issue
     const uint32_t idesc_s = tc::idesc_f16(128, 128, false, false, false);
     const uint32_t idesc_o = tc::idesc_f16(128, 128, false, false, true);   // V: tokens are the contraction
@@ -1055,9 +1056,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
       cp_wait<0>();
       __syncwarp();
     }
-  } else {
+  } else if (warp < kTcDeq + kTcSoft) {
     // ------------------------------------------------ softmax and output
-    const int qq = warp & 3, x = (warp - 1 - kTcDeq) >> 2;   // TMEM lane quarter; tiles of this parity
+    const int qq = warp & 3, x = (warp - kTcDeq) >> 2;   // TMEM lane quarter; tiles of this parity
     const int r = qq * 32 + lane;
     const uint32_t lane_base = (uint32_t)(qq * 32) << 16;
     const uint32_t s_at = tmem + lane_base + 128u * x, o_at = tmem + lane_base + o_col;
@@ -1246,13 +1247,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == kTcDeq) tc::tmem_dealloc(tmem, 512);
+  if (warp == kTcMma) tc::tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ merging the partials
 // One warp per output row and `hpw` query heads of it, lane: four channels.  Writes y as fp16 into the output product's B
 // tiles; rows of no sequence and the tiles' padding rows are zero.
-__global__ void __launch_bounds__(256) k_tree_combine(TreeMma a, int rows_pad, int NB, int KT, int hpw) {
+__global__ void __launch_bounds__(256, 6) k_tree_combine(TreeMma a, int rows_pad, int NB, int KT, int hpw) {
   const LayerView& v = a.v;
   const TreeArgs& t = a.t;
   const int lane = threadIdx.x & 31;
@@ -1422,7 +1423,7 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
                                                                                : launch_bits<0>(L, a, p, s);
   if (e != cudaSuccess) return e;
   // a warp per head while that fills the SMs at most twice; else a row's heads share their row's lookups
-  const int hpw = (long long)p.rows_pad * v.H <= 128LL * num_sms() ? 1 : 8;
+  const int hpw = (long long)p.rows_pad * v.H <= 128LL * num_sms() ? 1 : 4;
   const long long warps = (long long)p.rows_pad * ((v.H + hpw - 1) / hpw);
   e = launch_k(k_tree_combine, (unsigned)((warps * 32 + 255) / 256), 256, 0, s, true, a, p.rows_pad, p.NB, L->Kp / 64, hpw);
   if (e != cudaSuccess) return e;
