@@ -171,8 +171,14 @@ def _table(page_table, batch: int = 0):
 
 
 def _stream(stream) -> int:
+    """Handle of the given stream, or of torch's current one."""
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # without building a Stream object, which takes as long as a launch (3 us)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch._C._cuda_getDevice())
+        return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
