@@ -1271,6 +1271,7 @@ __global__ void __launch_bounds__(256, 6) k_tree_combine(TreeMma a, int rows_pad
   const long long U = a.w.unit_off[t.batch], We = workers_used(a, U);
   const long long u0 = live ? a.w.unit_off[b] : 0, i0 = live ? a.w.item_off[b] : 0;
   const int nt = row / NB, br = row % NB;
+  const bool small = U * We < (1ll << 32);
   tc::grid_wait_prev();
   for (int h = h0; h < min(v.H, h0 + hpw); ++h) {
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1278,7 +1279,15 @@ __global__ void __launch_bounds__(256, 6) k_tree_combine(TreeMma a, int rows_pad
       const int g = h / v.group_q, rr = (row - sq.off) * v.group_q + h % v.group_q;
       const int blk = g * nrb + rr / a.rb, r = rr % a.rb;
       const long long lo = u0 + (long long)blk * units, hi = lo + units - 1;
-      const long long w0 = ((lo + 1) * We - 1) / U, w1 = ((hi + 1) * We - 1) / U;   // the warps of the first, last unit
+      // the warps of the first and the last unit (divisions in 32 bits where they fit: a quarter of the instructions)
+      long long w0, w1;
+      if (small) {
+        w0 = ((uint32_t)(lo + 1) * (uint32_t)We - 1u) / (uint32_t)U;
+        w1 = ((uint32_t)(hi + 1) * (uint32_t)We - 1u) / (uint32_t)U;
+      } else {
+        w0 = ((lo + 1) * We - 1) / U;
+        w1 = ((hi + 1) * We - 1) / U;
+      }
       const long long base = i0 + blk;
       float m = -FLT_MAX, l = 0.f;
       for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, a.w.pm[(base + w) * a.rb + r]);

@@ -246,7 +246,7 @@ class Layer:
         self.free()
 
     def free(self) -> None:
-        if getattr(self, "_h", None):
+        if getattr(self, "_h", None) and _lib is not None:   # (gone at interpreter exit)
             _lib.starkv_free_layer(self._h)
             self._h = None
 
