@@ -114,7 +114,8 @@ __device__ __forceinline__ int warp_find(const T* off, int n, long long x, int l
 
 // ------------------------------------------------------------------ queries and the work list
 // Blocks (row, head group): norm, rotation, softmax scale * log2(e) of one query row per warp, rounded to fp16 (to a
-// bf16 pair high + low for bf16 caches, whose products then carry 16 bits).  The last block row: prefix sums.
+// bf16 pair high + low for bf16 caches, whose products then carry 16 bits, like the weights: one bf16 weight alone made the
+// outputs' error 2.2e-3 instead of 1.7e-3).  The last block row: prefix sums.
 // ORDER (4-bit codes): 0 = channels in order; 1, 2 = every eight in the order 0 4 1 5 2 6 3 7 in which the nibble masks give
 // them, with 1/16 for the odd ones (1: k_tree_mma, which meets 16 u there) or without (2: k_tree_tc).
 template <int BITS, int ORDER>
@@ -548,24 +549,25 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
           }
       }
       // ---- P (tokens r, r + 8 by query rows 2 j, + 1), transposed into the operand of the values: tokens 2 j .., row r
-      uint32_t pb[NT][2];
+      uint32_t pb[NT][QP][2];   // bf16: a high and a low part, like the queries
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float e0 = ex2(S[n][0] - m[n][0]), e1 = ex2(S[n][1] - m[n][1]);
         const float e2 = ex2(S[n][2] - m[n][0]), e3 = ex2(S[n][3] - m[n][1]);
         if constexpr (BITS == 0) {
           const uint32_t x = b2(e0, e1), y = b2(e2, e3);
-          // the sum is over the rounded weights, so that they add up to one
-          l[n][0] += __uint_as_float(x << 16) + __uint_as_float(y << 16);
-          l[n][1] += __uint_as_float(x & 0xFFFF0000u) + __uint_as_float(y & 0xFFFF0000u);
-          pb[n][0] = transpose8(x);
-          pb[n][1] = transpose8(y);
+          auto lo16 = [](uint32_t z) { return __uint_as_float(z << 16); };
+          auto hi16 = [](uint32_t z) { return __uint_as_float(z & 0xFFFF0000u); };
+          pb[n][0][0] = transpose8(x);
+          pb[n][0][1] = transpose8(y);
+          pb[n][1][0] = transpose8(b2(e0 - lo16(x), e1 - hi16(x)));
+          pb[n][1][1] = transpose8(b2(e2 - lo16(y), e3 - hi16(y)));
         } else {
-          l[n][0] += e0 + e2;
-          l[n][1] += e1 + e3;
-          pb[n][0] = transpose8(h2(e0, e1));
-          pb[n][1] = transpose8(h2(e2, e3));
+          pb[n][0][0] = transpose8(h2(e0, e1));
+          pb[n][0][1] = transpose8(h2(e2, e3));
         }
+        l[n][0] += e0 + e2;
+        l[n][1] += e1 + e3;
       }
       // ---- values: tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9, channels 32 c + 4 r .. + 3
       if constexpr (BITS == 0) {
@@ -593,10 +595,12 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
           const uint32_t v1[4] = {__byte_perm(x[0].y, x[1].y, 0x5410), __byte_perm(x[0].y, x[1].y, 0x7632),
                                   __byte_perm(x[2].y, x[3].y, 0x5410), __byte_perm(x[2].y, x[3].y, 0x7632)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_b(Y[n][2 * c], v0, pb[n][0], pb[n][1], Y[n][2 * c]);
-            mma_b(Y[n][2 * c + 1], v1, pb[n][0], pb[n][1], Y[n][2 * c + 1]);
-          }
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int part = 0; part < QP; ++part) {
+              mma_b(Y[n][2 * c], v0, pb[n][part][0], pb[n][part][1], Y[n][2 * c]);
+              mma_b(Y[n][2 * c + 1], v1, pb[n][part][0], pb[n][part][1], Y[n][2 * c + 1]);
+            }
         }
         if (tail) {
           bad = __reduce_or_sync(0xffffffffu, bad);
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint32_t ps0 = hmul2(pb[n][0], sc0), ps1 = hmul2(pb[n][1], sc1);
+            const uint32_t ps0 = hmul2(pb[n][0][0], sc0), ps1 = hmul2(pb[n][0][1], sc1);
             mma_h(Y[n][2 * c], v0, ps0, ps1, Y[n][2 * c]);
             mma_h(Y[n][2 * c + 1], v1, ps0, ps1, Y[n][2 * c + 1]);
           }

@@ -380,7 +380,9 @@ STARKV_API starkv_status starkv_cache_read(const starkv_layer* layer, const void
  *   workspace: starkv_tree_workspace_bytes(layer, batch, max_pages * 16, n_nodes, max_nodes) bytes.
  * A sequence with more than max_nodes nodes, or whose rows or slots leave
  * [0, n_nodes) or the page table, sets STARKV_DEV_BAD_POSITION and its rows are
- * zero; a node_off that decreases does so for every row.  The call reads
+ * zero; a node_off that decreases does so for every row.
+ * What lies in slots that a node does not see does not reach it, NaN included;
+ * a stored value that is not finite makes the nodes that see it NaN.  The call reads
  * hist, node_off and mask on the device only, so it can be captured and
  * replayed with other contents.
  */

@@ -412,6 +412,50 @@ def test_tree_masked_nodes_hold_nan():
     check_tree(args["out"].to(torch.float64).cpu(), want, "bf16")
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_tree_nan_reaches_only_the_nodes_that_see_it(what):
+    p = Plain(4, 2, 128, 0)
+    sees = [{0}, {0, 1}, {0, 2}, {0, 2, 3}, {0, 1, 4}]
+    for side in (0, 1):
+        got, want, c, args = run_tree(p, [21], [5], [sees])
+        K, V = c.K[0][21 + 2:21 + 3].clone(), c.V[0][21 + 2:21 + 3].clone()
+        (K if side == 0 else V)[0, :, 7] = what
+        R.put(c.pages, c.pt[0, 1:2], torch.tensor([7]), K, V, 0, p.dt)
+        p.L.tree_attn(**dict(args, pool=c.upload()))
+        out = args["out"].to(torch.float64).cpu()
+        check_tree(out[[0, 1, 4]], want[[0, 1, 4]], "bf16")
+        if not (side == 0 and what == float("inf")):           # (q times an infinite key may be minus infinity: weight 0)
+            assert torch.all(torch.isnan(out[[2, 3]]))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 128), ("bf16", 64)])
+def test_tree_plain_layer_of_load_factors(dtype, d):
+    """Uncompressed layers without serving options: a chain of nodes is the decode of each prefix."""
+    g = torch.Generator().manual_seed(0)
+    H, hkv, D, dt = 8, 2, 96, dt_of(dtype)
+    W = [(torch.randn(*s, generator=g) / s[0] ** 0.5).to(dt).cuda() for s in ((D, hkv * d), (D, hkv * d), (H * d, D))]
+    cfg = sk().LayerConfig(hidden=D, n_heads=H, n_kv_heads=hkv, head_dim=d, dtype=dtype, rope=True, plain=True)
+    L = sk().load_factors(cfg, W[0], None, W[1], None, W[2])
+    n, T = 5, 40
+    c = GpuCache(L, [T + n] * n)
+    x = torch.randn(T + n, 2 * hkv * d, generator=g).numpy()
+    for b in range(n):
+        c.append_latents(b, [x[:, :d], x[:, d:2 * d], x[:, 2 * d:]])
+    q = torch.randn(n, H, d, generator=g).to(dt).cuda()
+    out, want = (torch.empty(n, D, dtype=dt, device="cuda") for _ in range(2))
+    mp = c.page_table.shape[1]
+    ws = torch.empty(max(L.tree_workspace_bytes(1, mp * 16, n, n), L.workspace_bytes(n, mp * 16)), dtype=torch.uint8,
+                     device="cuda")
+    L.tree_attn(c.pool, c.n_pages, c.page_table[:1], i32([T]), i32([0, n]), q, out, ws, max_nodes=n,
+                q_pos=i32(range(T, T + n)))
+    L.decode(c.pool, c.n_pages, c.page_table, i32(range(T + 1, T + n + 1)), q, want, ws)
+    assert L.sync_status() == 0
+    a, b = out.to(torch.float64).cpu(), want.to(torch.float64).cpu()
+    # each side within its own bound of the definition: sqrt(2) * 1.7e-3 in bf16, two times 4e-5 in fp32
+    lim = 3e-3 if dtype == "bf16" else 8e-5
+    assert torch.linalg.norm(a - b) <= lim * torch.linalg.norm(b)
+
+
 @pytest.mark.parametrize("bits", [0, 4])
 def test_tree_bad_counts_and_pages(bits):
     """A sequence that does not fit its slots or max_nodes gives zero rows and a flag; the others are right."""
@@ -468,7 +512,8 @@ def test_decode_quantised(bits, H, hkv):
             c.fill(b, n)
     q = p.r(torch.randn(7, H, 128, generator=torch.Generator().manual_seed(1)))
     ws = torch.empty(p.L.workspace_bytes(7, c.pt.shape[1] * 16), dtype=torch.uint8, device="cuda").random_(0, 255)
-    for pos in (None, [3, 5, 9, 16, 10000, 1, 2499]):
+    for pos, path in ((None, 0), ([3, 5, 9, 16, 10000, 1, 2499], 0), (None, 1)):
+        p.L.set_decode_path(path)
         out = torch.empty(7, p.hidden, dtype=p.dt, device="cuda")
         p.L.decode(c.upload(), c.n_pages, c.pt_d, i32(lens), q.to(p.dt).cuda(), out, ws,
                    q_pos=None if pos is None else i32(pos))
@@ -478,7 +523,8 @@ def test_decode_quantised(bits, H, hkv):
         check_tree(out.to(torch.float64).cpu(), want, "bf16")
         assert torch.all(out[0] == 0)
     assert p.L.sync_status() == 0
-    p.L.decode(c.pool, c.n_pages, c.pt_d, i32([-1] + lens[1:6] + [5000]), q.to(p.dt).cuda(), out, ws, q_pos=i32(pos))
+    p.L.set_decode_path(0)
+    p.L.decode(c.pool, c.n_pages, c.pt_d, i32([-1] + lens[1:6] + [5000]), q.to(p.dt).cuda(), out, ws)
     assert p.L.sync_status() == 2
 
 
@@ -653,6 +699,40 @@ def test_speculative_rounds(bits, dtype):
         qx = p.norm_rope(q[b:b + 1], p.wq, torch.tensor([lens[b]]))
         see = torch.ones(1, lens[b] + 1, dtype=torch.bool)
         check_tree(out[b:b + 1].to(torch.float64).cpu(), R.attention(qx, K, V, see, d ** -0.5) @ p.W_o, dtype)
+    assert p.L.sync_status() == 0
+
+
+@pytest.mark.parametrize("bits", [0, 8, 4])
+def test_calls_on_two_streams(bits):
+    """Two calls at once on one layer, each with its own cache and workspace."""
+    p = Plain(4, 2, 128, bits)
+    runs = [run_tree(p, [700 + 40 * k, 33], [9, 20 + k], None, seed=k) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for (_, _, _, args), s in zip(runs, streams):
+            args["out"].zero_()
+        torch.cuda.synchronize()
+        for (_, _, _, args), s in zip(runs, streams):
+            p.L.tree_attn(**args, stream=s)
+        torch.cuda.synchronize()
+        for got, want, _, args in runs:
+            assert torch.equal(args["out"].to(torch.float64).cpu(), got)
+    assert p.L.sync_status() == 0
+
+
+@pytest.mark.parametrize("bits,n,hist", [(8, 40, 3000), (4, 300, 1000), (0, 33, 500)])
+def test_prefill_quantised(bits, n, hist):
+    """starkv_prefill_attn after a history: the definition's causal attention over the stored values."""
+    p = Plain(4, 2, 128, bits)
+    c = p.cache([hist + n])
+    c.fill(0, hist + n)
+    q = p.r(torch.randn(n, 4, 128, generator=torch.Generator().manual_seed(3)))
+    out = torch.empty(n, p.hidden, dtype=p.dt, device="cuda")
+    ws = torch.empty(p.L.workspace_bytes(1, c.pt.shape[1] * 16, n), dtype=torch.uint8, device="cuda")
+    p.L.prefill(c.upload(), c.n_pages, c.pt_d, [hist], [n], q.to(p.dt).cuda(), out, ws)
+    qx = p.norm_rope(q, p.wq, torch.arange(n) + hist)
+    see = torch.arange(hist + n)[None] <= torch.arange(n)[:, None] + hist
+    check_tree(out.to(torch.float64).cpu(), R.attention(qx, c.K[0], c.V[0], see, 128 ** -0.5) @ p.W_o, "bf16")
     assert p.L.sync_status() == 0
 
 
