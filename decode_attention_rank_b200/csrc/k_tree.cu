@@ -1255,16 +1255,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
 }
 
 // ------------------------------------------------------------------ merging the partials
-// One warp per output row and `hpw` query heads of it, lane: four channels.  Writes y as fp16 into the output product's B
-// tiles; rows of no sequence and the tiles' padding rows are zero.
-__global__ void __launch_bounds__(256, 6) k_tree_combine(TreeMma a, int rows_pad, int NB, int KT, int hpw) {
+// One warp per output row and HPW query heads of it, lane: four channels; the first partials of all its heads are asked for
+// together.  Writes y as fp16 into the output product's B tiles; rows of no sequence and the tiles' padding rows are zero.
+template <int HPW>
+__global__ void __launch_bounds__(256, HPW == 1 ? 6 : 4) k_tree_combine(TreeMma a, int rows_pad, int NB, int KT) {
   const LayerView& v = a.v;
   const TreeArgs& t = a.t;
   const int lane = threadIdx.x & 31;
   const long long id = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-  const int parts = (v.H + hpw - 1) / hpw;
+  const int parts = (v.H + HPW - 1) / HPW;
   if (id >= (long long)rows_pad * parts) return;
-  const int row = (int)(id / parts), h0 = (int)(id % parts) * hpw;
+  const int row = (int)(id / parts), h0 = (int)(id % parts) * HPW;
   // (what the query kernel wrote is complete: the attention kernel lets this one start only after its own wait for it)
   tc::grid_launch_next();
   const int b = row < t.n_nodes ? a.w.row_b[row] : -1;
@@ -1274,46 +1275,57 @@ __global__ void __launch_bounds__(256, 6) k_tree_combine(TreeMma a, int rows_pad
   const int nrb = (sq.cnt * v.group_q + a.rb - 1) / a.rb, units = (sq.hist + sq.cnt + a.unit - 1) / a.unit;
   const long long U = a.w.unit_off[t.batch], We = workers_used(a, U);
   const long long u0 = live ? a.w.unit_off[b] : 0, i0 = live ? a.w.item_off[b] : 0;
-  const int nt = row / NB, br = row % NB;
   const bool small = U * We < (1ll << 32);
-  tc::grid_wait_prev();
-  for (int h = h0; h < min(v.H, h0 + hpw); ++h) {
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-      const int g = h / v.group_q, rr = (row - sq.off) * v.group_q + h % v.group_q;
-      const int blk = g * nrb + rr / a.rb, r = rr % a.rb;
-      const long long lo = u0 + (long long)blk * units, hi = lo + units - 1;
-      // the warps of the first and the last unit (divisions in 32 bits where they fit: a quarter of the instructions)
-      long long w0, w1;
-      if (small) {
-        w0 = ((uint32_t)(lo + 1) * (uint32_t)We - 1u) / (uint32_t)U;
-        w1 = ((uint32_t)(hi + 1) * (uint32_t)We - 1u) / (uint32_t)U;
-      } else {
-        w0 = ((lo + 1) * We - 1) / U;
-        w1 = ((hi + 1) * We - 1) / U;
-      }
-      const long long base = i0 + blk;
-      float m = -FLT_MAX, l = 0.f;
-      for (long long w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, a.w.pm[(base + w) * a.rb + r]);
+  long long at[HPW];   // the head's first partial
+  int n[HPW];          // and how many
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll 4
-      for (long long w = w0; w <= w1; ++w) {
-        const long long p = (base + w) * a.rb + r;
-        const float4 x = *reinterpret_cast<const float4*>(a.w.pY + p * 128 + lane * 4);
-        const float f = ex2(a.w.pm[p] - m);
-        l += f * a.w.pl[p];
-        y.x += f * x.x;
-        y.y += f * x.y;
-        y.z += f * x.z;
-        y.w += f * x.w;
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: zero; NaN stays
-      y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+  for (int i = 0; i < HPW; ++i) {
+    at[i] = n[i] = 0;
+    const int h = h0 + i;
+    if (!live || h >= v.H) continue;
+    const int g = h / v.group_q, rr = (row - sq.off) * v.group_q + h % v.group_q;
+    const int blk = g * nrb + rr / a.rb;
+    const long long lo = u0 + (long long)blk * units, hi = lo + units - 1;
+    // the warps of the first and the last unit (divisions in 32 bits where they fit: a quarter of the instructions)
+    long long w0, w1;
+    if (small) {
+      w0 = ((uint32_t)(lo + 1) * (uint32_t)We - 1u) / (uint32_t)U;
+      w1 = ((uint32_t)(hi + 1) * (uint32_t)We - 1u) / (uint32_t)U;
+    } else {
+      w0 = ((lo + 1) * We - 1) / U;
+      w1 = ((hi + 1) * We - 1) / U;
     }
+    at[i] = (i0 + blk + w0) * a.rb + rr % a.rb;
+    n[i] = (int)(w1 - w0) + 1;
+  }
+  tc::grid_wait_prev();
+  float m[HPW], l[HPW];
+  float4 y[HPW];
+#pragma unroll
+  for (int i = 0; i < HPW; ++i) {
+    m[i] = n[i] ? a.w.pm[at[i]] : 0.f;
+    l[i] = n[i] ? a.w.pl[at[i]] : 0.f;
+    y[i] = n[i] ? *reinterpret_cast<const float4*>(a.w.pY + at[i] * 128 + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < HPW; ++i) {
+    const int h = h0 + i;
+    if (h >= v.H) break;
+#pragma unroll 4
+    for (int k = 1; k < n[i]; ++k) {
+      const long long p = at[i] + (long long)k * a.rb;
+      const float4 x = *reinterpret_cast<const float4*>(a.w.pY + p * 128 + lane * 4);
+      const float mk = a.w.pm[p], lk = a.w.pl[p];
+      const float mn = fmaxf(m[i], mk), f0 = ex2(m[i] - mn), f = ex2(mk - mn);
+      m[i] = mn;
+      l[i] = l[i] * f0 + lk * f;
+      y[i] = make_float4(y[i].x * f0 + x.x * f, y[i].y * f0 + x.y * f, y[i].z * f0 + x.z * f, y[i].w * f0 + x.w * f);
+    }
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];   // a row that sees nothing: zero; NaN stays
     const uint32_t k = (uint32_t)(h * 128 + lane * 4), c = k & 63u;
-    uint8_t* tile = (uint8_t*)a.w.y + ((size_t)nt * KT + (k >> 6)) * (size_t)NB * 128;
-    *reinterpret_cast<uint2*>(tile + tc::sw128((uint32_t)br, c >> 3) + (c & 7u) * 2u) = make_uint2(h2(y.x, y.y), h2(y.z, y.w));
+    uint8_t* tile = (uint8_t*)a.w.y + ((size_t)(row / NB) * KT + (k >> 6)) * (size_t)NB * 128;
+    *reinterpret_cast<uint2*>(tile + tc::sw128((uint32_t)(row % NB), c >> 3) + (c & 7u) * 2u) =
+        make_uint2(h2(y[i].x * inv, y[i].y * inv), h2(y[i].z * inv, y[i].w * inv));
   }
 }
 
@@ -1436,9 +1448,10 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
                                                                                : launch_bits<0>(L, a, p, s);
   if (e != cudaSuccess) return e;
   // a warp per head while that fills the SMs at most twice; else a row's heads share their row's lookups
-  const int hpw = (long long)p.rows_pad * v.H <= 128LL * num_sms() ? 1 : 4;
-  const long long warps = (long long)p.rows_pad * ((v.H + hpw - 1) / hpw);
-  e = launch_k(k_tree_combine, (unsigned)((warps * 32 + 255) / 256), 256, 0, s, true, a, p.rows_pad, p.NB, L->Kp / 64, hpw);
+  const bool few = (long long)p.rows_pad * v.H <= 128LL * num_sms();
+  const long long warps = (long long)p.rows_pad * (few ? v.H : (v.H + 3) / 4);
+  e = launch_k(few ? k_tree_combine<1> : k_tree_combine<4>, (unsigned)((warps * 32 + 255) / 256), 256, 0, s, true, a, p.rows_pad,
+               p.NB, L->Kp / 64);
   if (e != cudaSuccess) return e;
   const int32_t* n_rows = t.lens ? nullptr : t.node_off + t.batch;
   if (p.full) return launch_out_full(L, a.w.y, t.n_nodes, t.out, n_rows, s, true);
