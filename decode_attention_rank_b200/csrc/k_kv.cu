@@ -14,7 +14,7 @@
 
 #include <type_traits>
 
-#include "starkv_internal.cuh"
+#include "tc_common.cuh"
 
 namespace starkv {
 
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
   const int i = blockIdx.x, nw = blockDim.x >> 5, b0 = blockIdx.y * nw * per, b1 = min(groups, b0 + nw * per);
   const int nq = a.q ? (v.H + RPW - 1) / RPW : 0, nk = a.k ? (v.Hkv + RPW - 1) / RPW : 0;
   const int c = lane % LPR, rr = lane / LPR;
+  tc::grid_wait_prev();
   // the rows of this warp's next group, asked for ahead
   uint4 rl, rh;
   auto fetch = [&](int g) {
@@ -468,8 +469,8 @@ cudaError_t launch_qkv_d(const KvArgs& a, cudaStream_t s) {
   // Few: a row group per warp, the token over several CTAs, for latency.
   const bool many = (long long)a.n * groups > 64LL * num_sms();
   const int nw = std::min(many ? 4 : NW, groups), per = many ? (groups + nw - 1) / nw : 1;
-  k_qkv<T, D, BITS><<<dim3((unsigned)a.n, (unsigned)((groups + nw * per - 1) / (nw * per))), 32 * nw, 0, s>>>(a, groups, per);
-  return cudaGetLastError();
+  return launch_k(k_qkv<T, D, BITS>, dim3((unsigned)a.n, (unsigned)((groups + nw * per - 1) / (nw * per))), 32 * nw, 0, s, true,
+                  a, groups, per);
 }
 
 template <typename T>
@@ -505,6 +506,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) k_read8(KvArgs a, int chunks_
   const long long i = (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
   if (i >= a.n) return;
   const int cph = CPH ? CPH : v.d / 8, d = CPH ? CPH * 8 : v.d;
+  tc::grid_wait_prev();
   const int keys = v.Hkv * cph, chunks = 2 * keys;
   const int e0 = blockIdx.y * chunks_per_warp, e1 = min(chunks, e0 + chunks_per_warp);
   int slot = 0;
@@ -663,12 +665,13 @@ constexpr int kAccThreads = 256;
 template <int BITS>
 __global__ void __launch_bounds__(kAccThreads) k_accept_plain(AcceptArgs a, int pieces) {
   constexpr int PER = BITS ? BITS / 4 : 1;                                     // pieces of one group (kv_bits)
-  constexpr int IT = kAccNodes * kAccPieces / kAccThreads;
+  constexpr int IT = kAccNodes * kAccPieces / kAccThreads, STEP = kAccPieces / IT;
   __shared__ long long src[kAccNodes], dst[kAccNodes];   // byte offset of the page (-1: nothing to move), per node
   __shared__ int ss[kAccNodes], ds[kAccNodes];           // slots; ss -1: cleared
   const LayerView& v = a.v;
   const int b = blockIdx.y;
   const bool first = blockIdx.x == 0;
+  tc::grid_wait_prev();
   const TreeSeq q = tree_seq(a.hist, a.node_off, b, a.n_nodes, a.max_nodes, a.max_pages * kPage, v.status,
                              first && threadIdx.x == 0);
   if (q.cnt <= 0) return;
@@ -701,51 +704,50 @@ __global__ void __launch_bounds__(kAccThreads) k_accept_plain(AcceptArgs a, int 
       ds[threadIdx.x] = t;
     }
     __syncthreads();
+    // a thread keeps its node and takes every STEP-th piece
+    const int k = threadIdx.x / PER % kAccNodes;
+    const int pc0 = blockIdx.x * kAccPieces + threadIdx.x / (PER * kAccNodes) * PER + threadIdx.x % PER;
+    const bool move = dst[k] >= 0, keep = move && ss[k] >= 0;
+    const uint8_t* sp = a.pool + (keep ? src[k] : 0);
+    uint8_t* dp = a.pool + (move ? dst[k] : 0);
+    const int st = ss[k], dt = ds[k];
     uint4 x[IT];
-    __half sc[IT];
-    // piece of (block offset of slot 0, bytes from slot to slot, scale of slot 0)
-    auto where = [&](int pc, long long* at, int* step, long long* scale) {
-      if constexpr (BITS != 0) {
-        constexpr int GB = kPage * 4 * BITS;
-        const int g = pc / PER, gd = v.d / 32, kb = gd * (32 + GB);   // group of the token: keys by head, then values
-        const bool val = g >= v.Hkv * gd;
-        const int gl = val ? g - v.Hkv * gd : g % gd;
-        const long long blk = (long long)(val ? v.Hkv : g / gd) * kb;
-        *scale = pc % PER == 0 ? blk + gl * 32 : -1;
-        *at = blk + (val ? v.Hkv * v.d : v.d) + (long long)gl * GB + (pc % PER) * 16;
-        *step = 4 * BITS;
-      } else {
-        const int row = v.d * v.es, c = pc * 16, keys = v.Hkv * row;   // bytes of one head's row
-        const bool val = c >= keys;
-        *scale = -1;
-        *at = val ? (long long)kPage * keys + (c - keys) : (long long)(c / row) * kPage * row + c % row;
-        *step = val ? keys : row;
-      }
-    };
+    uint16_t sc[IT];
+    int at[IT], scale[IT];   // the piece's offset in the page for slot 0, and its group's scale's (-1: none)
+    const int row = v.d * v.es, keys = v.Hkv * row;
+    constexpr int GB = kPage * 4 * BITS;
+    const int gd = v.d / 32, kb = gd * (32 + GB), hk = v.Hkv * gd;
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      const int e = it * kAccThreads + threadIdx.x;
-      const int pl = e % PER, k = (e / PER) % kAccNodes, pc = blockIdx.x * kAccPieces + e / (PER * kAccNodes) * PER + pl;
+      const int pc = pc0 + it * STEP;
       x[it] = make_uint4(0, 0, 0, 0);
-      sc[it] = __float2half_rn(0.f);
-      if (pc >= pieces || src[k] < 0 || ss[k] < 0) continue;
-      long long at, scale;
-      int step;
-      where(pc, &at, &step, &scale);
-      x[it] = *reinterpret_cast<const uint4*>(a.pool + src[k] + at + (long long)ss[k] * step);
-      if (scale >= 0) sc[it] = reinterpret_cast<const __half*>(a.pool + src[k] + scale)[ss[k]];
+      sc[it] = 0;
+      int step = 4 * BITS;
+      if constexpr (BITS != 0) {
+        const int g = pc / PER;   // group of the token: keys by head, then values
+        const bool val = g >= hk;
+        const int gl = val ? g - hk : g % gd, blk = (val ? v.Hkv : g / gd) * kb;
+        scale[it] = pc % PER == 0 ? blk + gl * 32 : -1;
+        at[it] = blk + (val ? v.Hkv * v.d : v.d) + gl * GB + (pc % PER) * 16;
+      } else {
+        const int c = pc * 16;    // byte of the slot: the heads' key rows, then the value row
+        const bool val = c >= keys;
+        scale[it] = -1;
+        step = val ? keys : row;
+        at[it] = val ? kPage * keys + (c - keys) : c / row * kPage * row + c % row;
+      }
+      if (keep && pc < pieces) {
+        x[it] = *reinterpret_cast<const uint4*>(sp + at[it] + st * step);
+        if (scale[it] >= 0) sc[it] = reinterpret_cast<const uint16_t*>(sp + scale[it])[st];
+      }
+      at[it] += dt * step;
     }
     __syncthreads();
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      const int e = it * kAccThreads + threadIdx.x;
-      const int pl = e % PER, k = (e / PER) % kAccNodes, pc = blockIdx.x * kAccPieces + e / (PER * kAccNodes) * PER + pl;
-      if (pc >= pieces || dst[k] < 0) continue;
-      long long at, scale;
-      int step;
-      where(pc, &at, &step, &scale);
-      *reinterpret_cast<uint4*>(a.pool + dst[k] + at + (long long)ds[k] * step) = x[it];
-      if (scale >= 0) reinterpret_cast<__half*>(a.pool + dst[k] + scale)[ds[k]] = sc[it];
+      if (!move || pc0 + it * STEP >= pieces) continue;
+      *reinterpret_cast<uint4*>(dp + at[it]) = x[it];
+      if (scale[it] >= 0) reinterpret_cast<uint16_t*>(dp + scale[it])[dt] = sc[it];
     }
     __syncthreads();
   }
@@ -851,7 +853,7 @@ cudaError_t launch_qkv(const KvArgs& a, bool f32, cudaStream_t s) {
 namespace {
 
 template <typename TO, int BITS>
-void read_plain(const KvArgs& a, void* out, cudaStream_t s) {
+cudaError_t read_plain(const KvArgs& a, void* out, cudaStream_t s) {
   const int chunks = 2 * a.v.Hkv * (a.v.d / 8);
   // few tokens: a row is spread over several warps, down to one round of a warp's unrolled loads
   const long long rows = ((long long)a.n + kReadWarps - 1) / kReadWarps;
@@ -859,14 +861,9 @@ void read_plain(const KvArgs& a, void* out, cudaStream_t s) {
   const int parts = (int)std::max(1LL, std::min((long long)(chunks + least - 1) / least, 8LL * num_sms() / rows));
   const int per = ((chunks + parts - 1) / parts + 31) / 32 * 32;
   const dim3 grid((unsigned)rows, (unsigned)((chunks + per - 1) / per));
-  if (a.v.d == 128)
-    k_read8<TO, BITS, 16><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
-  else if (a.v.d == 64)
-    k_read8<TO, BITS, 8><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
-  else if (a.v.d == 256)
-    k_read8<TO, BITS, 32><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
-  else
-    k_read8<TO, 0, 0><<<grid, 32 * kReadWarps, 0, s>>>(a, per, (TO*)out);
+  auto* kernel = a.v.d == 128 ? k_read8<TO, BITS, 16>
+                 : a.v.d == 64 ? k_read8<TO, BITS, 8> : a.v.d == 256 ? k_read8<TO, BITS, 32> : k_read8<TO, 0, 0>;
+  return launch_k(kernel, grid, 32 * kReadWarps, 0, s, true, a, per, (TO*)out);
 }
 
 }  // namespace
@@ -877,11 +874,10 @@ cudaError_t launch_cache_read(const KvArgs& a, void* out, cudaStream_t s) {
   // eight channels a lane: rows of whole 8-channel chunks
   if (v.plain && v.d % 8 == 0) {
     if (f32)
-      v.kv_bits == 8 ? read_plain<float, 8>(a, out, s) : v.kv_bits == 4 ? read_plain<float, 4>(a, out, s)
+      return v.kv_bits == 8 ? read_plain<float, 8>(a, out, s) : v.kv_bits == 4 ? read_plain<float, 4>(a, out, s)
                                                                         : read_plain<float, 0>(a, out, s);
-    else
-      v.kv_bits == 8 ? read_plain<__nv_bfloat16, 8>(a, out, s) : v.kv_bits == 4 ? read_plain<__nv_bfloat16, 4>(a, out, s)
-                                                                                : read_plain<__nv_bfloat16, 0>(a, out, s);
+    return v.kv_bits == 8 ? read_plain<__nv_bfloat16, 8>(a, out, s) : v.kv_bits == 4 ? read_plain<__nv_bfloat16, 4>(a, out, s)
+                                                                                     : read_plain<__nv_bfloat16, 0>(a, out, s);
   } else {
     const unsigned gw = (unsigned)(((long long)a.n * v.L * 32 + 255) / 256);
     if (f32) k_read_any<float><<<gw, 256, 0, s>>>(a, (float*)out);
@@ -901,10 +897,8 @@ cudaError_t launch_accept(const starkv_layer* L, uint8_t* pool, long long n_page
     const int pieces = slot_bytes / 16;
     const dim3 grid((pieces + kAccPieces - 1) / kAccPieces, batch);
     if (batch <= 65535) {
-      if (v.kv_bits == 8) k_accept_plain<8><<<grid, kAccThreads, 0, s>>>(a, pieces);
-      else if (v.kv_bits == 4) k_accept_plain<4><<<grid, kAccThreads, 0, s>>>(a, pieces);
-      else k_accept_plain<0><<<grid, kAccThreads, 0, s>>>(a, pieces);
-      return cudaGetLastError();
+      return launch_k(v.kv_bits == 8 ? k_accept_plain<8> : v.kv_bits == 4 ? k_accept_plain<4> : k_accept_plain<0>, grid,
+                      kAccThreads, 0, s, true, a, pieces);
     }
   }
   const long long warps = (long long)batch * a.n_grp;

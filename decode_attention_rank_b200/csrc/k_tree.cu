@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(128) k_tree_prep(TreeMma a) {
   const LayerView& v = a.v;
   const TreeArgs& t = a.t;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  tc::grid_wait_prev();
   if (blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y != 0) return;
     // one warp walks the batch 32 sequences at a time
@@ -1394,16 +1395,13 @@ cudaError_t launch_mma(const TreeMma& a, cudaStream_t s) {
 template <int BITS>
 cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cudaStream_t s) {
   const LayerView& v = L->view;
+  cudaError_t e;
   const dim3 pgrid(a.t.n_nodes + 1, (v.H + kTreeWarps - 1) / kTreeWarps);
   if constexpr (BITS == 4) {
-    if (p.tc)
-      k_tree_prep<BITS, 2><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
-    else
-      k_tree_prep<BITS, 1><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
+    e = launch_k(p.tc ? k_tree_prep<BITS, 2> : k_tree_prep<BITS, 1>, pgrid, 32 * kTreeWarps, 0, s, true, a);
   } else {
-    k_tree_prep<BITS, 0><<<pgrid, 32 * kTreeWarps, 0, s>>>(a);
+    e = launch_k(k_tree_prep<BITS, 0>, pgrid, 32 * kTreeWarps, 0, s, true, a);
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (BITS != 0 && p.tc) {
     constexpr int B = BITS == 0 ? 8 : BITS;
