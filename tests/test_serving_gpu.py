@@ -702,6 +702,93 @@ def test_speculative_rounds(bits, dtype):
     assert p.L.sync_status() == 0
 
 
+@pytest.mark.parametrize("bits", [0, 8])
+def test_pages_beyond_4_gib(bits):
+    """Append, read, attention and accept on pages whose byte offsets pass 32 bits."""
+    H = hkv = 32
+    p = Plain(H, hkv, 128, bits)
+    n_pages = (9 << 29) // p.L.page_bytes + 8                   # 4.5 GiB
+    pool = torch.empty(n_pages * p.L.page_bytes, dtype=torch.uint8, device="cuda")
+    pt = i32([[n_pages - 1, n_pages - 4, n_pages - 3], [n_pages - 6, 0, n_pages - 2]])
+    g = torch.Generator().manual_seed(0)
+    n = 48
+    x = p.r(torch.randn(2 * n, 3 * H * 128, generator=g))
+    seq, slots = i32([0] * n + [1] * n), i32(list(range(n)) * 2)
+    xd = x.to(p.dt).cuda()
+    parts = [xd[:, i * H * 128:(i + 1) * H * 128] for i in range(3)]
+    p.L.append_qkv(pool, n_pages, pt, seq, slots, None, *parts[1:])
+    out = torch.empty(2 * n, 2 * H * 128, dtype=p.dt, device="cuda")
+    p.L.cache_read(pool, n_pages, pt, seq, slots, out)
+    K = p.norm_rope(x[:, H * 128:2 * H * 128].reshape(-1, H, 128), p.wk, torch.arange(n).repeat(2))
+    V = R.stored(x[:, 2 * H * 128:], bits, p.dt).reshape(-1, H, 128)
+    if bits:
+        K = R.stored(K, bits, p.dt)
+        assert torch.equal(out[:, :H * 128].cpu(), K.reshape(2 * n, -1).to(torch.float32).to(p.dt))
+    else:
+        close_rows(out[:, :H * 128].reshape(-1, H, 128), K, pair_size(K), p.dt)
+    assert torch.equal(out[:, H * 128:].cpu(), V.reshape(2 * n, -1).to(torch.float32).to(p.dt))
+    k, hist = 7, n - 7
+    q = p.r(torch.randn(2 * k, H, 128, generator=g))
+    y = torch.empty(2 * k, p.hidden, dtype=p.dt, device="cuda")
+    ws = torch.empty(p.L.tree_workspace_bytes(2, 48, 2 * k, k), dtype=torch.uint8, device="cuda")
+    p.L.tree_attn(pool, n_pages, pt, i32([hist, hist]), i32([0, k, 2 * k]), q.to(p.dt).cuda(), y, ws, max_nodes=k)
+    kd = out[:, :H * 128].to(torch.float64).cpu().reshape(-1, H, 128)
+    see = torch.arange(n)[None] <= torch.arange(k)[:, None] + hist
+    want = torch.cat([R.attention(q[b * k:(b + 1) * k], (K if bits else kd)[b * n:(b + 1) * n], V[b * n:(b + 1) * n], see,
+                                  128 ** -0.5) @ p.W_o for b in range(2)])
+    check_tree(y.to(torch.float64).cpu(), want, "bf16")
+    p.L.tree_accept(pool, n_pages, pt, i32([hist, hist]), i32([0, k, 2 * k]), i32([1, 3, 6, 0, 0, 0, 0] * 2), i32([3, 3]),
+                    max_nodes=k)
+    after = torch.empty_like(out)
+    p.L.cache_read(pool, n_pages, pt, seq, slots, after)
+    for b in range(2):
+        o = b * n
+        assert torch.equal(after[o:o + hist], out[o:o + hist])
+        assert torch.equal(after[o + hist:o + hist + 3], out[[o + hist + 1, o + hist + 3, o + hist + 6]])
+        assert torch.all(after[o + hist + 3:o + n] == 0)
+    assert p.L.sync_status() == 0
+
+
+@pytest.mark.parametrize("bits", [0, 8, 4])
+def test_append_and_read_captured(bits):
+    """One graph of append_qkv and cache_read, replayed with other rows and slots."""
+    p = Plain(4, 2, 128, bits)
+    c = p.cache([64, 64])
+    pool = c.upload()
+    n = 9
+    x = torch.zeros(n, 8 * 128, dtype=p.dt, device="cuda")
+    seq, slots = i32([0] * n), i32(range(n))
+    qo, out = torch.empty(n, 512, dtype=p.dt, device="cuda"), torch.empty(n, 512, dtype=p.dt, device="cuda")
+
+    def calls():
+        p.L.append_qkv(pool, c.n_pages, c.pt_d, seq, slots, x[:, :512], x[:, 512:768], x[:, 768:], q_out=qo)
+        p.L.cache_read(pool, c.n_pages, c.pt_d, seq, slots, out)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for k in range(3):
+        xv = p.r(torch.randn(n, 1024, generator=torch.Generator().manual_seed(k)))
+        sl = torch.randperm(64, generator=torch.Generator().manual_seed(k))[:n]
+        x.copy_(xv.to(p.dt))
+        slots.copy_(i32(sl))
+        seq.copy_(i32([k % 2] * n))
+        graph.replay()
+        torch.cuda.synchronize()
+        K = p.norm_rope(xv[:, 512:768].reshape(n, 2, 128), p.wk, sl)
+        w = p.norm_rope(xv[:, :512].reshape(n, 4, 128), p.wq, sl)
+        close_rows(qo.reshape(n, 4, 128), w, pair_size(w), p.dt)
+        if bits:
+            kv = torch.cat((R.stored(K, bits, p.dt).reshape(n, -1), R.stored(xv[:, 768:], bits, p.dt)), -1)
+            assert torch.equal(out.cpu(), kv.to(torch.float32).to(p.dt))
+        else:
+            close_rows(out[:, :256].reshape(n, 2, 128), K, pair_size(K), p.dt)
+    assert p.L.sync_status() == 0
+    del graph
+
+
 @pytest.mark.parametrize("bits", [0, 8, 4])
 def test_calls_on_two_streams(bits):
     """Two calls at once on one layer, each with its own cache and workspace."""
