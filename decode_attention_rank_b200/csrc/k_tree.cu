@@ -76,12 +76,17 @@ struct TreeMma {
   int workers;           // warps (k_tree_mma) or CTAs (k_tree_tc) that share the units
   int rb;                // rows of a row block: 16, or 128
   int unit;              // tokens of a unit: a page, or a tile of 128
-  int min_units;
+  int min_units;         // least units of a worker's run
+  float run_scale;       // and sqrt(run_scale * units of an average row block)
 };
 
-// How a call's units are dealt: worker w takes units [w U / We, (w + 1) U / We).
+// How a call's units are dealt: worker w takes units [w U / We, (w + 1) U / We).  Short calls use fewer workers than there are:
+// a run costs its units, the merge a row block's partials, so long row blocks are cut into the fewer the longer they are.  One
+// sequence, 4 drafts, 8 KV heads, 8 bits: of 8000 tokens 63 us with runs of 2 pages and 47 with this rule, of 333 tokens 25 either way.
 __device__ __forceinline__ long long workers_used(const TreeMma& a, long long U) {
-  return min((long long)a.workers, max(1ll, U / a.min_units));
+  const long long items = max(1ll, a.w.item_off[a.t.batch]);
+  const int run = max(a.min_units, (int)__fsqrt_rn((float)(U / items) * a.run_scale));
+  return min((long long)a.workers, max(1ll, U / run));
 }
 
 __device__ __forceinline__ TreeSeq seq_of(const TreeArgs& t, int b, uint32_t* status, bool flag) {
@@ -1346,13 +1351,15 @@ struct TreePlan {
   int workers, rb, nt;   // nt: 8-row tiles of a row block of k_tree_mma
 };
 
-// Rows per sequence and KV head from which the 128-row kernel is taken.
+// Rows per sequence and KV head from which the 128-row kernel is taken.  16 sequences of 4K: 24 rows, 8 bits, 8 KV heads 72 us by
+// k_tree_mma, 73 by k_tree_tc, 32 KV heads 188 and 225; 28 rows 82 and 74; 32 rows, 32 KV heads 244 and 219.
 constexpr int kTcFrom = 25;
 
 TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
   const LayerView& v = L->view;
   TreePlan p;
-  // Up to 256 rows the output product reads W_o once in an even split over the SMs; beyond, 128 x 128 tiles fill them.
+  // Up to 256 rows the output product reads W_o once in an even split over the SMs; beyond, 128 x 128 tiles fill them (a whole call
+  // over a short cache: 242 rows 41 us against 54, 400 rows 68 against 66, 820 rows 131 against 90).
   p.full = n_nodes > 256;
   p.NB = p.full ? 128 : outproj_nb(n_nodes);
   p.rows_pad = (n_nodes + p.NB - 1) / p.NB * p.NB;
@@ -1445,6 +1452,7 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
   a.rb = p.rb;
   a.unit = p.tc ? kTcTok : kPage;
   a.min_units = p.tc ? 1 : kMinUnits;
+  a.run_scale = p.tc ? 0.f : 0.25f;   // (a tile of k_tree_tc costs as much as merging a dozen partials)
   cudaError_t e = v.kv_bits == 8 ? launch_bits<8>(L, a, p, s) : v.kv_bits == 4 ? launch_bits<4>(L, a, p, s)
                                                                                : launch_bits<0>(L, a, p, s);
   if (e != cudaSuccess) return e;
