@@ -401,4 +401,96 @@ size_t rows_tiles_bytes(int rows, int K) {
   return (size_t)((rows + NB - 1) / NB) * ((K + 63) / 64) * NB * 128;
 }
 
+namespace {
+
+// out[row][n] = sum_k y[row][k] M[k][n] for up to 8 NT rows, in one launch: a CTA takes 16 outputs, its 8 warps every eighth
+// k-tile each (m16n8k16: 16 outputs by 8 rows), and adds their sums in a fixed order through shared memory.  The tiles of
+// M go from global memory straight into operand registers: a lane reads whole 16-byte chunks (8 k) of its rows, and the
+// same chunks of y, so any order of k is the same on both sides.  M's first tiles are asked for before the wait for y.
+// Bound: M's bytes (33.5 MB for 4096 x 4096) and latency.  7 rows 9.8 us, against 12 + 6 by k_outproj_tc and its reduction; a tree of
+// 7 over 333 tokens 29 -> 26 us.
+constexpr int kOsWarps = 8, kOsAhead = 4;   // k-tiles asked for at a time
+
+template <int NT, typename TO>
+__global__ void __launch_bounds__(32 * kOsWarps, 2) k_out_small(const uint8_t* __restrict__ M, const uint8_t* y, int NB, int KT,
+                                                                int rows, int n_valid, const int32_t* n_rows,
+                                                                TO* __restrict__ out) {
+  __shared__ float red[kOsWarps][16][8 * NT + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+  const int dt = blockIdx.x >> 3, ro = (blockIdx.x & 7) * 16;
+  const uint8_t* m = M + (size_t)dt * KT * 16384 + (size_t)(ro + r) * 128;
+  const int c0 = (j ^ r) << 4, c1 = ((j + 4) ^ r) << 4;   // this lane's two chunks of a row, swizzled
+  tc::grid_launch_next();
+  uint4 w[kOsAhead][4];
+  auto load_w = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kOsAhead; ++i) {
+      const int kt = (i0 + i) * kOsWarps + warp;
+      const uint8_t* p = m + (size_t)kt * 16384;
+      const bool in = kt < KT;
+      w[i][0] = in ? __ldg(reinterpret_cast<const uint4*>(p + c0)) : make_uint4(0, 0, 0, 0);
+      w[i][1] = in ? __ldg(reinterpret_cast<const uint4*>(p + 1024 + c0)) : make_uint4(0, 0, 0, 0);
+      w[i][2] = in ? __ldg(reinterpret_cast<const uint4*>(p + c1)) : make_uint4(0, 0, 0, 0);
+      w[i][3] = in ? __ldg(reinterpret_cast<const uint4*>(p + 1024 + c1)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load_w(0);
+  tc::grid_wait_prev();
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+  const int per = (KT + kOsWarps - 1) / kOsWarps;
+  for (int i0 = 0; i0 < per; i0 += kOsAhead) {
+#pragma unroll
+    for (int i = 0; i < kOsAhead; ++i) {
+      const int kt = (i0 + i) * kOsWarps + warp;
+      if (kt >= KT) break;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint8_t* yr = y + (size_t)kt * NB * 128 + n * 1024 + r * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 b = *reinterpret_cast<const uint4*>(yr + (h ? c1 : c0));
+          const uint4 &x = w[i][2 * h], &z = w[i][2 * h + 1];
+          const uint32_t a0[4] = {x.x, z.x, x.y, z.y}, a1[4] = {x.z, z.z, x.w, z.w};
+          asm volatile(
+              "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+              : "+f"(acc[n][0]), "+f"(acc[n][1]), "+f"(acc[n][2]), "+f"(acc[n][3])
+              : "r"(a0[0]), "r"(a0[1]), "r"(a0[2]), "r"(a0[3]), "r"(b.x), "r"(b.y));
+          asm volatile(
+              "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+              : "+f"(acc[n][0]), "+f"(acc[n][1]), "+f"(acc[n][2]), "+f"(acc[n][3])
+              : "r"(a1[0]), "r"(a1[1]), "r"(a1[2]), "r"(a1[3]), "r"(b.z), "r"(b.w));
+        }
+      }
+    }
+    if (i0 + kOsAhead < per) load_w(i0 + kOsAhead);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[warp][r + 8 * (e >> 1)][8 * n + 2 * j + (e & 1)] = acc[n][e];
+  __syncthreads();
+  if (n_rows) rows = min(rows, *n_rows);
+  for (int e = threadIdx.x; e < 128 * NT; e += 32 * kOsWarps) {
+    const int o = e & 15, row = e >> 4, d = blockIdx.x * 16 + o;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kOsWarps; ++k) s += red[k][o][row];
+    if (row < rows && d < n_valid) out[(size_t)row * n_valid + d] = (TO)s;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_out_small(const starkv_layer* L, const void* y_tiles, int rows, void* out, const int32_t* n_rows,
+                             cudaStream_t s) {
+  const int NB = outproj_nb(rows), KT = L->Kp / 64;
+  return launch_k(rows <= 8 ? k_out_small<1, __nv_bfloat16> : k_out_small<2, __nv_bfloat16>, L->Dp / 16, 32 * kOsWarps, 0, s,
+                  true, (const uint8_t*)L->M_T, (const uint8_t*)y_tiles, NB, KT, rows, L->view.D, n_rows,
+                  (__nv_bfloat16*)out);
+}
+
 }  // namespace starkv

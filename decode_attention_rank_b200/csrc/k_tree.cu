@@ -1463,6 +1463,7 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
                p.NB, L->Kp / 64);
   if (e != cudaSuccess) return e;
   const int32_t* n_rows = t.lens ? nullptr : t.node_off + t.batch;
+  if (t.n_nodes <= kOutSmallRows) return launch_out_small(L, a.w.y, t.n_nodes, t.out, n_rows, s);
   if (p.full) return launch_out_full(L, a.w.y, t.n_nodes, t.out, n_rows, s, true);
   return launch_outproj_tc(L, a.w.y, t.n_nodes, t.out, (float*)a.w.part, s, n_rows, true);
 }

@@ -306,6 +306,10 @@ cudaError_t launch_cache_read(const KvArgs& a, void* out, cudaStream_t s);
 cudaError_t launch_accept(const starkv_layer* L, uint8_t* pool, long long n_pages, const int32_t* pt, int max_pages,
                           int batch, const int32_t* hist, const int32_t* node_off, int n_nodes, int max_nodes,
                           const int32_t* acc, const int32_t* n_acc, cudaStream_t s);
+// out = y M of a bf16 layer for up to kOutSmallRows rows, y as launch_outproj_tc takes it: one launch, without a workspace.
+constexpr int kOutSmallRows = 16;
+cudaError_t launch_out_small(const starkv_layer* L, const void* y_tiles, int rows, void* out, const int32_t* n_rows,
+                             cudaStream_t s);
 // out = y W_o for many rows: y as fp16 tiles of 128 rows x 64 columns (head_dim 128).  n_rows (device, may be null): output
 // rows from *n_rows on are not written.
 cudaError_t launch_out_full(const starkv_layer* L, const void* yt, int rows, void* out, const int32_t* n_rows,
