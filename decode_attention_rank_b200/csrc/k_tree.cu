@@ -730,9 +730,10 @@ constexpr int kTcTile = 32768, kTcAtom = 16384;
 template <int BITS>
 struct TcFmt {
   static constexpr int KB = PageFmt<BITS>::KB, VS = PageFmt<BITS>::VS;
-  static constexpr int RAW = 8 * PageFmt<BITS>::STAGE;           // 34816 or 18432 bytes: the pages of a tile
-  static constexpr int RS = BITS == 8 ? 2 : 4;                   // tiles in flight
-  static constexpr size_t SMEM = 4 * (size_t)kTcTile + (size_t)RS * RAW + 1024;
+  static constexpr int ST = BITS == 0 ? 3 : 2;                                   // stages of K and V tiles
+  static constexpr int RAW = BITS == 0 ? 0 : 8 * PageFmt<BITS>::STAGE;           // 34816 or 18432 bytes: the pages of a tile
+  static constexpr int RS = BITS == 8 ? 2 : 4;                                   // tiles of codes in flight
+  static constexpr size_t SMEM = 2 * ST * (size_t)kTcTile + (size_t)RS * RAW + 1024;
 };
 
 // One CTA's run of units, a row block's tiles at a time; by a whole warp.
@@ -841,14 +842,6 @@ __device__ __forceinline__ void tmem_wait32(float* v) {
                  "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
                  "+f"(v[30]), "+f"(v[31])::"memory");
 }
-__device__ __forceinline__ void tmem_st16x(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st32x(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -887,15 +880,17 @@ template <int BITS>
 __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
   using F = TcFmt<BITS>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], q_full,
+  constexpr int ST = F::ST;
+  __shared__ __align__(8) uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], o_done[2], q_full,
       o_free, fin;
+  __shared__ uint16_t bad[ST][8];   // bf16: per page of a tile with drafted nodes, the tokens whose values are not finite
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
   __shared__ float xch[2][kTcRows], xl[2][kTcRows];   // by tile parity: row maxima handed on, and sums
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* K_s = smem;                      // two stages
-  uint8_t* V_s = smem + 2 * kTcTile;        // two stages
-  uint8_t* R_s = smem + 4 * kTcTile;        // raw pages
+  uint8_t* K_s = smem;
+  uint8_t* V_s = smem + ST * kTcTile;
+  uint8_t* R_s = smem + 2 * ST * kTcTile;   // codes
   const LayerView& v = a.v;
   const TreeArgs& t = a.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -909,11 +904,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
   wk.u = (long long)w * U / We;
   wk.u1 = (long long)(w + 1) * U / We;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < ST; ++s) {
       tc::mbar_init(&k_full[s], kTcDeq);
       tc::mbar_init(&k_empty[s], 1);
       tc::mbar_init(&v_full[s], kTcDeq);
       tc::mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&s_full[s], 1);
       // one barrier per tile parity, whose tiles belong to one half of the softmax warps
       tc::mbar_init(&p_full[s], kTcSoft / 2);
@@ -934,8 +931,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
 
   if (warp == kTcMma) {
     // ------------------------------------------------ MMA issue
-    const uint32_t idesc_s = tc::idesc_f16(128, 128, false, false, false);
-    const uint32_t idesc_o = tc::idesc_f16(128, 128, false, false, true);   // V: tokens are the contraction
+    const uint32_t idesc_s = tc::idesc_f16(128, 128, BITS == 0, false, false);
+    const uint32_t idesc_o = tc::idesc_f16(128, 128, BITS == 0, false, true);   // V: tokens are the contraction
+    constexpr int QP = BITS == 0 ? 2 : 1;   // bf16: Q and P as a high and a low part
     const uint64_t dk = tc::sdesc_sw128(tc::smem_u32(K_s), 0, 1024);
     const uint64_t dv = tc::sdesc_sw128(tc::smem_u32(V_s), kTcAtom, 1024);  // 64 channels to the next, 8 tokens to the next
     const uint32_t k_lo = tc::desc_lo(dk), k_hi = tc::desc_hi(dk), v_lo = tc::desc_lo(dv), v_hi = tc::desc_hi(dv);
@@ -946,18 +944,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
     bool ok = true;
     int jg = 0, n = 0;   // tiles and row blocks so far
     auto issue_s = [&](int j) -> bool {
-      const int s = j & 1;
-      if (!tc::mbar_wait_ab(&k_full[s], ((uint32_t)(j >> 1)) & 1u, v.status, &abort_flag)) return false;
+      const int s = j & 1, st = j % ST;
+      if (!tc::mbar_wait_ab(&k_full[st], ((uint32_t)(j / ST)) & 1u, v.status, &abort_flag)) return false;
       tc::tc_fence_after();
       // S buffer j & 1 is free: P(j - 2) V(j - 2), issued before, has read it by the time these run (a block's first two
       // tiles: the last block's products have completed, its softmax warps have said so by q_full)
-      const uint32_t d = tmem + (uint32_t)(s * 128), b = k_lo + (uint32_t)(s * kTcTile >> 4);
+      const uint32_t d = tmem + (uint32_t)(s * 128), b = k_lo + (uint32_t)(st * kTcTile >> 4);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts(leader, d, tmem + q_col + 8u * kk, b + (uint32_t)(kk >> 2) * (kTcAtom >> 4) + 2u * (kk & 3), k_hi, idesc_s,
-               kk ? 1u : 0u);
+      for (int part = 0; part < QP; ++part)
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(leader, d, tmem + q_col + 64u * part + 8u * kk, b + (uint32_t)(kk >> 2) * (kTcAtom >> 4) + 2u * (kk & 3), k_hi,
+                 idesc_s, (part | kk) ? 1u : 0u);
       commit(leader, &s_full[s]);
-      commit(leader, &k_empty[s]);
+      commit(leader, &k_empty[st]);
       return true;
     };
     while (ok && tc_next(a, wk, w, lane)) {
@@ -966,17 +966,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
       tc::tc_fence_after();
       ok = ok && issue_s(jg) && (nt == 1 || issue_s(jg + 1));
       for (int k = 0; ok && k < nt; ++k) {
-        const int j = jg + k, s = j & 1;
+        const int j = jg + k, s = j & 1, st = j % ST;
         if (k == 0 && !(ok = tc::mbar_wait_ab(&o_free, ((uint32_t)n & 1u) ^ 1u, v.status, &abort_flag))) break;
-        if (!(ok = tc::mbar_wait_ab(&v_full[s], ((uint32_t)(j >> 1)) & 1u, v.status, &abort_flag))) break;
+        if (!(ok = tc::mbar_wait_ab(&v_full[st], ((uint32_t)(j / ST)) & 1u, v.status, &abort_flag))) break;
         if (!(ok = tc::mbar_wait_ab(&p_full[s], ((uint32_t)(j >> 1)) & 1u, v.status, &abort_flag))) break;
         tc::tc_fence_after();
-        const uint32_t p = tmem + (uint32_t)(s * 128), b = v_lo + (uint32_t)(s * kTcTile >> 4);
+        const uint32_t p = tmem + (uint32_t)(s * 128), b = v_lo + (uint32_t)(st * kTcTile >> 4);
+        // P: 8 columns per 16 tokens; in two parts, 16 columns of the high, then 16 of the low one, per 32 tokens
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(leader, tmem + o_col, p + 8u * kk, b + (uint32_t)(kk * 2048 >> 4), v_hi, idesc_o, (k | kk) ? 1u : 0u);
+        for (int part = 0; part < QP; ++part)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(leader, tmem + o_col, p + (BITS == 0 ? 32u * (kk >> 1) + 8u * (kk & 1) + 16u * part : 8u * kk),
+                   b + (uint32_t)(kk * 2048 >> 4), v_hi, idesc_o, (k | part | kk) ? 1u : 0u);
         commit(leader, &o_done[s]);
-        commit(leader, &v_empty[s]);
+        commit(leader, &v_empty[st]);
         if (k + 2 < nt && !(ok = issue_s(j + 2))) break;
       }
       jg += nt;
@@ -986,6 +990,81 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
     if (!ok) abort_flag = 1;
     commit(leader, &fin);
     tc::mbar_wait(&fin, 0, v.status);   // every MMA has completed before the CTA may exit
+    __syncwarp();
+  } else if (BITS == 0 && warp < kTcDeq) {
+    // ------------------------------------------------ bf16: page `warp` of every tile, copied to its place in the tiles.  A tile
+    // is handed over after the copies of the next one, of whichever block, have been asked for.  (That waits for a stage whose
+    // products need no later tile than the one handed over last.)
+    bool ok = true;
+    int n = 0;
+    const int row0 = warp * 16;
+    auto at = [&](int e) { return (uint32_t)((e & 15) >> 3) * kTcAtom + tc::sw128((uint32_t)(row0 + (e >> 4)), (uint32_t)(e & 7)); };
+    int tokens = kTcTok;   // of this page of tile n - 1, which is to be handed over; beyond 16: all, before the drafted nodes
+    auto hand_over = [&]() {
+      const int st = (n - 1) % ST;
+      if (tokens < kTcTok) {
+        // a slot that some rows do not see must not reach them through 0 * NaN: values that are not finite, and slots without
+        // a token, enter as zero; the rows that see such a token become NaN in the softmax
+        unsigned odd = 0;
+#pragma unroll 1
+        for (int x = 0; x < 8; ++x) {
+          const int e = x * 32 + lane;
+          uint4* z = reinterpret_cast<uint4*>(V_s + (size_t)st * kTcTile + at(e));
+          const uint4 u = *z;
+          auto bad2 = [](uint32_t y) { return (y & 0x7F80u) == 0x7F80u || (y & 0x7F800000u) == 0x7F800000u; };
+          const bool out = (e >> 4) >= tokens, nan = bad2(u.x) || bad2(u.y) || bad2(u.z) || bad2(u.w);
+          if (out || nan) *z = make_uint4(0u, 0u, 0u, 0u);
+          if (!out && nan) odd |= 1u << (e >> 4);
+        }
+        odd = __reduce_or_sync(0xffffffffu, odd);
+        if (lane == 0) bad[st][warp] = (uint16_t)odd;
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&k_full[st]);
+        tc::mbar_arrive(&v_full[st]);
+      }
+    };
+    while (ok && tc_next(a, wk, w, lane)) {
+      const int32_t* pt = t.pt + (size_t)wk.b * t.max_pages;
+      const int pages = (wk.len + kPage - 1) / kPage;
+#pragma unroll 1
+      for (int k = wk.p0; k < wk.p1 && ok; ++k) {
+        const int st = n % ST, p = k * 8 + warp;
+        const uint32_t ph = (((uint32_t)(n / ST)) & 1u) ^ 1u;
+        const bool some = p < pages;   // past the sequence's pages the stage keeps what it held: those slots hold no token
+        const int page = some ? pt[p] : 0;
+        const bool live = some && page >= 0 && page < t.n_pages;
+        if (some && !live && lane == 0) atomicOr(v.status, kBadPage);
+        const uint8_t* base = t.pool + (size_t)(live ? page : 0) * v.page_bytes;
+        const uint8_t* ks = base + (size_t)wk.g * F::KB;
+        const uint8_t* vs = base + (size_t)v.Hkv * F::KB + (size_t)wk.g * 256;
+        const uint32_t kd = tc::smem_u32(K_s + (size_t)st * kTcTile), vd = tc::smem_u32(V_s + (size_t)st * kTcTile);
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_ab(&k_empty[st], ph, v.status, &abort_flag));
+        if (ok && some) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) cp16(kd + at(x * 32 + lane), ks + (x * 32 + lane) * 16, live);
+        }
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_ab(&v_empty[st], ph, v.status, &abort_flag));
+        if (ok && some) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int e = x * 32 + lane;
+            cp16(vd + at(e), vs + (size_t)(e >> 4) * v.Hkv * 256 + (e & 15) * 16, live);
+          }
+        }
+        cp_commit();
+        if (n > 0) {
+          cp_wait<1>();
+          hand_over();
+        }
+        ++n;
+        tokens = (k + 1) * kTcTok > wk.sq.hist ? min(wk.len - (k * kTcTok + row0), 16) : kTcTok;
+      }
+    }
+    cp_wait<0>();
+    if (ok && n > 0) hand_over();
     __syncwarp();
   } else if (warp < kTcDeq) {
     // ------------------------------------------------ dequantisation: page `warp` of every tile
@@ -1034,7 +1113,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
           const uint8_t* sc = (side ? raw + F::KB : raw) + 32 * gr + 2 * sl;
           const uint8_t* cd = (side ? raw + F::KB + F::VS : raw + 128) + gr * (64 * BITS) + sl * (4 * BITS);
           // all loads first: the compiler keeps a load behind a store that may alias it
-          uint4 code[2][BITS / 4];
+          uint4 code[2][BITS ? BITS / 4 : 1];
           uint32_t scale[2];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -1086,18 +1165,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
       const int node = row / v.group_q;
       // ---- this row's Q: 64 of its channels (32 columns) into TMEM.  The last block's MMAs have completed (o_done).
       {
-        uint32_t qv[32];
-        const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)a.w.q +
-                                                          ((size_t)(wk.sq.off + node) * v.H + wk.g * v.group_q + row % v.group_q) * 128 + 64 * x);
+#pragma unroll 1
+        for (int part = 0; part < (BITS == 0 ? 2 : 1); ++part) {
+          uint32_t qv[32];
+          const uint4* src = reinterpret_cast<const uint4*>(
+              (const uint16_t*)a.w.q + (((size_t)part * t.n_nodes + wk.sq.off + node) * v.H + wk.g * v.group_q + row % v.group_q) * 128 + 64 * x);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 z = row < wk.R ? src[c] : make_uint4(0, 0, 0, 0);
-          qv[4 * c] = z.x;
-          qv[4 * c + 1] = z.y;
-          qv[4 * c + 2] = z.z;
-          qv[4 * c + 3] = z.w;
+          for (int c = 0; c < 8; ++c) {
+            const uint4 z = row < wk.R ? src[c] : make_uint4(0, 0, 0, 0);
+            qv[4 * c] = z.x;
+            qv[4 * c + 1] = z.y;
+            qv[4 * c + 2] = z.z;
+            qv[4 * c + 3] = z.w;
+          }
+          tmem_st32x(tmem + lane_base + q_col + 64u * part + 32u * x, qv);
         }
-        tmem_st32x(tmem + lane_base + q_col + 32u * x, qv);
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
@@ -1112,11 +1194,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
         if (warp_live) {   // (also after an abort: the two warps of a quarter meet at their barriers, over old columns)
           const int t0 = (wk.p0 + k) * kTcTok;
           const bool tail = t0 + kTcTok > wk.sq.hist;   // the tile holds drafted nodes or unused slots
+          bool odd = false;   // bf16: the row sees a value that is not finite
           if (tail) {   // what a row does not see becomes -infinity in TMEM
+            // (long complete: the wait is for what the copying warps wrote to bad)
+            if constexpr (BITS == 0) tc::mbar_wait_ab(&k_full[j % ST], ((uint32_t)(j / ST)) & 1u, v.status, &abort_flag);
 #pragma unroll 1
             for (int h = 0; h < 4; ++h) {
               float s[32];
               const uint32_t see = row < wk.R ? vis32(t, wk.sq.off + node, node, wk.sq.cnt, t0 + 32 * h - wk.sq.hist) : 0u;
+              if constexpr (BITS == 0) odd = odd || (see & ((uint32_t)bad[j % ST][2 * h] | (uint32_t)bad[j % ST][2 * h + 1] << 16)) != 0u;
               tmem_ld32x(s_at + 32u * h, s);
               tmem_wait32(s);
 #pragma unroll
@@ -1178,33 +1264,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
               tc::tmem_st_wait();
             }
           }
-          // P over columns of S that have been read: 16 columns of pairs for 32 of scores
+          // P over columns of S that have been read: 16 columns of pairs for 32 of scores (bf16: 16 and 16)
           unsigned long long l2[4] = {0ull, 0ull, 0ull, 0ull};   // packed pairs of sums
           const unsigned long long nm = pack2(-m_used, -m_used);
-          auto put = [&](uint32_t at, const float* s) {
-            uint32_t p2[16];
+          auto put = [&](int h, const float* s) {   // piece h
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float2 d = unpack2(add2(pack2(s[c], s[c + 1]), nm));
-              const float e0 = ex2(d.x), e1 = ex2(d.y);
-              l2[(c >> 1) & 3] = add2(l2[(c >> 1) & 3], pack2(e0, e1));
-              p2[c / 2] = h2(e0, e1);
+            for (int c0 = 0; c0 < 32; c0 += 16) {
+              uint32_t p2[8], q2[8];
+#pragma unroll
+              for (int c = c0; c < c0 + 16; c += 2) {
+                const float2 d = unpack2(add2(pack2(s[c], s[c + 1]), nm));
+                const float e0 = ex2(d.x), e1 = ex2(d.y);
+                l2[(c >> 1) & 3] = add2(l2[(c >> 1) & 3], pack2(e0, e1));
+                if constexpr (BITS == 0) {
+                  const uint32_t z = b2(e0, e1);
+                  p2[(c - c0) / 2] = z;
+                  q2[(c - c0) / 2] = b2(e0 - __uint_as_float(z << 16), e1 - __uint_as_float(z & 0xFFFF0000u));
+                } else {
+                  p2[(c - c0) / 2] = h2(e0, e1);
+                }
+              }
+              tc::tmem_st8(s_at + (BITS == 0 ? 32u : 16u) * h + c0 / 2, p2);
+              if constexpr (BITS == 0) tc::tmem_st8(s_at + 32u * h + 16u + c0 / 2, q2);
             }
-            tmem_st16x(at, p2);
           };
           tmem_wait32(s0);
           tmem_ld32x(s_at + 32u, s1);
-          put(s_at, s0);
+          put(0, s0);
           tmem_wait32(s1);
           tmem_ld32x(s_at + 64u, s0);
-          put(s_at + 16u, s1);
+          put(1, s1);
           tmem_wait32(s0);
           tmem_ld32x(s_at + 96u, s1);
-          put(s_at + 32u, s0);
+          put(2, s0);
           tmem_wait32(s1);
-          put(s_at + 48u, s1);
+          put(3, s1);
           const float2 ls = unpack2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
           l += ls.x + ls.y;
+          if (BITS == 0 && odd) l = NAN;
           tc::tmem_st_wait();
         }
         tc::tc_fence_before();
@@ -1354,6 +1451,7 @@ struct TreePlan {
 // Rows per sequence and KV head from which the 128-row kernel is taken.  16 sequences of 4K: 24 rows, 8 bits, 8 KV heads 72 us by
 // k_tree_mma, 73 by k_tree_tc, 32 KV heads 188 and 225; 28 rows 82 and 74; 32 rows, 32 KV heads 244 and 219.
 constexpr int kTcFrom = 25;
+constexpr int kTcFromBf16 = 17;
 
 TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
   const LayerView& v = L->view;
@@ -1364,7 +1462,7 @@ TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes)
   p.NB = p.full ? 128 : outproj_nb(n_nodes);
   p.rows_pad = (n_nodes + p.NB - 1) / p.NB * p.NB;
   // row blocks, one more per sequence for what its last block leaves empty
-  p.tc = v.kv_bits != 0 && max_nodes * v.group_q >= kTcFrom;
+  p.tc = max_nodes * v.group_q >= (v.kv_bits ? kTcFrom : kTcFromBf16);
   // the fewest 8-row tiles that hold the rows, up to three (registers; bf16: two, and as many blocks as it takes)
   const int rows = max_nodes * v.group_q;
   p.nt = rows <= 8 ? 1 : rows <= 16 || v.kv_bits == 0 ? 2 : 3;
@@ -1413,10 +1511,9 @@ cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cu
     e = launch_k(k_tree_prep<BITS, 0>, pgrid, 32 * kTreeWarps, 0, s, true, a);
   }
   if (e != cudaSuccess) return e;
-  if (BITS != 0 && p.tc) {
-    constexpr int B = BITS == 0 ? 8 : BITS;
-    if ((e = set_smem_limit((const void*)k_tree_tc<B>, TcFmt<B>::SMEM)) != cudaSuccess) return e;
-    return launch_k(k_tree_tc<B>, a.workers, kTcThreads, TcFmt<B>::SMEM, s, true, a);
+  if (p.tc) {
+    if ((e = set_smem_limit((const void*)k_tree_tc<BITS>, TcFmt<BITS>::SMEM)) != cudaSuccess) return e;
+    return launch_k(k_tree_tc<BITS>, a.workers, kTcThreads, TcFmt<BITS>::SMEM, s, true, a);
   }
   if (p.nt == 1) return launch_mma<BITS, 1>(a, s);
   if (p.nt == 2 || BITS == 0) return launch_mma<BITS, 2>(a, s);

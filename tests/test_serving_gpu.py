@@ -428,6 +428,38 @@ def test_tree_nan_reaches_only_the_nodes_that_see_it(what):
             assert torch.all(torch.isnan(out[[2, 3]]))
 
 
+@pytest.mark.parametrize("group,n,hist", [(2, 20, 37), (4, 33, 300), (8, 64, 128)])
+def test_tree_of_many_rows_and_values_that_are_not_finite(group, n, hist):
+    """As the two tests above, with more rows per KV head, nodes over several tiles, and rows that see nothing."""
+    p = Plain(2 * group, 2, 128, 0)
+    sees = R.random_tree(random.Random(n), n)[0]
+    hidden = {5, n - 2}
+    sees = [s - hidden for s in sees]
+    got, want, c, args = run_tree(p, [hist, 0], [n, n], [sees, [set() if i % 3 == 0 else s for i, s in enumerate(sees)]])
+    check_tree(got, want, "bf16")
+    assert torch.all(got[n::3][:n // 3] == 0)
+    nan = torch.full((1, 2, 128), float("nan"), dtype=torch.float64)
+    for b, h in enumerate((hist, 0)):
+        for j in [*sorted(hidden), *range(n, n + 9)]:                 # and slots past the nodes
+            if (h + j) // 16 < c.pt.shape[1]:
+                R.put(c.pages, c.pt[b, (h + j) // 16:(h + j) // 16 + 1], torch.tensor([(h + j) % 16]), nan, nan, 0, p.dt)
+    clean = c.upload().clone()
+    p.L.tree_attn(**dict(args, pool=clean))
+    check_tree(args["out"].to(torch.float64).cpu(), want, "bf16")
+    for what, side in ((float("nan"), 0), (float("nan"), 1), (float("inf"), 1)):
+        K, V = c.K[0][hist + 2:hist + 3].clone(), c.V[0][hist + 2:hist + 3].clone()
+        (V if side else K)[0, :, 7] = what
+        at = c.pt[0, (hist + 2) // 16:(hist + 2) // 16 + 1], torch.tensor([(hist + 2) % 16])
+        R.put(c.pages, *at, K, V, 0, p.dt)
+        p.L.tree_attn(**dict(args, pool=c.upload()))
+        R.put(c.pages, *at, c.K[0][hist + 2:hist + 3], c.V[0][hist + 2:hist + 3], 0, p.dt)
+        out = args["out"].to(torch.float64).cpu()
+        see = torch.tensor([2 in s for s in sees] + [False] * n)
+        assert see.any() and torch.all(torch.isnan(out[see]))
+        check_tree(out[~see], want[~see], "bf16")
+    assert p.L.sync_status() == 0
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 128), ("bf16", 64)])
 def test_tree_plain_layer_of_load_factors(dtype, d):
     """Uncompressed layers without serving options: a chain of nodes is the decode of each prefix."""
