@@ -722,6 +722,11 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
 // Measured: 64 trees of 24 over 8K, 4 bits, 32 heads on 8 KV heads in 354 us (blocks of 16 rows in k_tree_mma's way: 1,213 us). Bound
 // by issue slots, about 1,800 a scheduler and tile; the products alone would take 1,300 cycles a tile.
 // TMEM: S in two 128-column buffers, O in 256 .. 383, Q in 384 .. 447.  Units of work: tiles, dealt to the CTAs as above.
+// bf16 caches: K and V are operands as they lie, so warps 0 - 7 copy them straight into three stages of tiles.  Q and P enter as
+// a high and a low bf16 part (one rounding of P to bf16 would show in the output), in TMEM columns 384 .. 511 and in place, 16
+// columns of each part per 32 tokens: twice the products, some 2,600 of 3,800 cycles a tile.  16 sequences of 4K, 64 rows on each
+// of 8 KV heads: 95 us (k_tree_mma: 156); 24 of 10000, 512 rows on 4: 441 (1,589).  The scores of the next block during a block's
+// output (its Q asked for early) spilt registers and took 7 % longer.
 constexpr int kTcDeq = 8, kTcSoft = 8;
 constexpr int kTcMma = 19;             // (the scheduler of lane quarter 3, whose rows are used least; warps 16 - 18 only wait)
 constexpr int kTcThreads = 32 * (kTcMma + 1);
@@ -1450,8 +1455,10 @@ struct TreePlan {
 
 // Rows per sequence and KV head from which the 128-row kernel is taken.  16 sequences of 4K: 24 rows, 8 bits, 8 KV heads 72 us by
 // k_tree_mma, 73 by k_tree_tc, 32 KV heads 188 and 225; 28 rows 82 and 74; 32 rows, 32 KV heads 244 and 219.
+// bf16: 20 rows 85 and 85, 32 KV heads 282 and 267; 24 rows 95 and 84, 297 and 264; 28 rows 97 and 85; 64 rows 153 and 92; but 64
+// short sequences of 500 tokens 86 and 115 at 20 rows, 93 and 117 at 28, 137 and 132 at 64 (8 bits, 28 rows, by k_tree_tc: 104).
+// Lengths are known on the device only, so one number serves both.
 constexpr int kTcFrom = 25;
-constexpr int kTcFromBf16 = 17;
 
 TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
   const LayerView& v = L->view;
@@ -1462,7 +1469,7 @@ TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes)
   p.NB = p.full ? 128 : outproj_nb(n_nodes);
   p.rows_pad = (n_nodes + p.NB - 1) / p.NB * p.NB;
   // row blocks, one more per sequence for what its last block leaves empty
-  p.tc = max_nodes * v.group_q >= (v.kv_bits ? kTcFrom : kTcFromBf16);
+  p.tc = max_nodes * v.group_q >= kTcFrom;
   // the fewest 8-row tiles that hold the rows, up to three (registers; bf16: two, and as many blocks as it takes)
   const int rows = max_nodes * v.group_q;
   p.nt = rows <= 8 ? 1 : rows <= 16 || v.kv_bits == 0 ? 2 : 3;

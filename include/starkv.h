@@ -382,8 +382,8 @@ STARKV_API starkv_status starkv_cache_read(const starkv_layer* layer, const void
  * [0, n_nodes) or the page table, sets STARKV_DEV_BAD_POSITION and its rows are
  * zero; a node_off that decreases does so for every row.
  * What lies in slots that a node does not see does not reach it, NaN included;
- * a stored value that is not finite makes the nodes that see it NaN.  The call reads
- * hist, node_off and mask on the device only, so it can be captured and
+ * a stored value that is not finite makes what the nodes that see it give infinite or
+ * NaN.  The call reads hist, node_off and mask on the device only, so it can be captured and
  * replayed with other contents.
  */
 STARKV_API starkv_status starkv_tree_attn(const starkv_layer* layer, const void* pool, int64_t n_pages,
