@@ -11,16 +11,20 @@
 //            4-bit codes in a word's high nibbles come out as 1024 + 16 u, their q is 1/16).  A group's accumulator starts
 //            at -sum_c q_c (1024 + 2^(b-1)), so it ends at sum_c q_c (u - 2^(b-1)); then S += scale[token][group] * it.
 //            |offset| is below 40 times the sum, whose fp32 rounding stays below 2^-17 of q's length times a code.
-//   values   Y^T = V^T P^T.  The scale belongs to (token, group): P, transposed by one movmatrix per 8 tokens, is multiplied
-//            by it in fp16, per group of 32 channels, and the codes enter as exact integers (the offset taken off by one
-//            packed subtraction; it cannot be folded into the accumulator here, whose sum over thousands of tokens would
-//            cancel).
-// Channels within a group may enter a contraction in any order, so each lane reads runs of bytes: eight channels of a
-// token for the scores, four channels of four tokens for the values.
+//   values   Y^T = V^T P^T.  P is transposed by one movmatrix per 8 tokens.  The codes become exact integers (the offset taken
+//            off by one packed subtraction; it cannot be folded into the accumulator here, whose sum over thousands of tokens
+//            would cancel) and are multiplied by their token's scale in fp16.  |code * scale| <= 32768 fits, and as every scale
+//            is a multiple of 2^-24 so is every product: the rounding is 2^-11 of it at most, however small the scale.  (P * scale
+//            instead, with 2 NT products a group for 8, leaves fp16 at both ends: 2^7 * 4681, the largest scale of 4 bits, is
+//            infinite, and a weight 2^-12 of the largest is lost beside values of 1e-3.  It took 97.4 us for one token each of 16
+//            sequences of 4K over 4 bits and 32 heads against 98.4, 133.3 against 131.9 for 16, and over 8 bits 101.0 against
+//            100.7 and 129.9 against 129.5.)
+// Channels may be dealt to a contraction in any order, so each lane reads runs of bytes: eight channels of a token for the
+// scores, 8 bytes of each of four tokens for the values (bf16: four channels).
 //
 // Running maximum and sum are per row in registers.  m is the row's maximum less 3 (log2 units) and moves only when a
-// score passes m + 7: p = 2^(s - m) <= 2^7, times a scale <= 258 stays inside fp16 (65504), while the largest weight
-// seen is at least 8, so that weights down to 2^-17 of it keep full precision.
+// score passes m + 7: p = 2^(s - m) <= 2^7, while the largest weight seen is at least 8, so that weights down to 2^-17 of it
+// keep full precision in fp16.
 //
 // Work split: the units (sequence, KV head, row block, page) of the whole call, in this order, are dealt to the resident
 // warps in equal runs; a warp writes one partial (m, l, Y) per row block that its run touches, and k_tree_combine
@@ -419,7 +423,9 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
           bias[n][c][1] = __shfl_sync(0xffffffffu, s, 8 * j + 4);
         }
     }
-    float Y[NT][8][4];   // m-tile 2 c + i: rows r, r + 8 = channels 32 c + 4 r + 2 i, + 1; columns: query rows 2 j, + 1
+    // columns: query rows 2 j, + 1.  Rows r, r + 8 of an m-tile are channels: of 2 c + i, 32 c + 4 r + 2 i and + 1 (bf16); of 4 c + i,
+    // 64 c + 8 r + 2 i and + 1 (8 bits); of i, 16 r + 2 i and + 1 (4 bits)
+    float Y[NT][8][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -622,57 +628,70 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
       } else {
         const uint8_t* sv = st + F::KB;
         const uint8_t* cv = sv + F::VS;
+        // A lane reads 8 bytes of a token: 8 channels of group 2 c + r / 4, or 16 of group r / 2.  Half of the lanes take the tokens
+        // of a pair in the other order, so that the warp's reads do not meet in a bank.
+        constexpr int LPG = BITS == 8 ? 4 : 2;   // lanes r to a group
+        const int swap = BITS == 8 ? j >> 1 : (r >> 1) & 1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t sc0 = *reinterpret_cast<const uint32_t*>(sv + c * 32 + j * 4);        // scales of tokens 2 j, 2 j + 1
-          uint32_t sc1 = *reinterpret_cast<const uint32_t*>(sv + c * 32 + 16 + j * 4);   // and 8 on
+        for (int c = 0; c < LPG / 2; ++c) {
+          const int gr = 8 / LPG * c + r / LPG;
+          uint32_t sc0 = *reinterpret_cast<const uint32_t*>(sv + gr * 32 + j * 4);        // scales of tokens 2 j, 2 j + 1
+          uint32_t sc1 = *reinterpret_cast<const uint32_t*>(sv + gr * 32 + 16 + j * 4);   // and 8 on
           if (tail) {
             // unused slots may hold any bytes: no scale that is not a number meets a weight of zero
             const int n0 = len - p * kPage - 2 * j, n1 = n0 - 8;   // tokens of the pair on
             sc0 = n0 >= 2 ? sc0 : n0 == 1 ? sc0 & 0xFFFFu : 0u;
             sc1 = n1 >= 2 ? sc1 : n1 == 1 ? sc1 & 0xFFFFu : 0u;
           }
-          uint32_t v0[4], v1[4];
-          if constexpr (BITS == 8) {
-            uint32_t x[4];
+          uint2 w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              x[i] = *reinterpret_cast<const uint32_t*>(cv + c * 512 + (2 * j + (i & 1) + 8 * (i >> 1)) * 32 + r * 4);
-            const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), b01 = __byte_perm(x[0], x[1], 0x7362);
-            const uint32_t a23 = __byte_perm(x[2], x[3], 0x5140), b23 = __byte_perm(x[2], x[3], 0x7362);
-            constexpr uint32_t off = 0x64806480u, ex = 0x64646464u;   // 1152, 1152
-            v0[0] = hsub2(__byte_perm(a01, ex, 0x4140), off);
-            v0[1] = hsub2(__byte_perm(a01, ex, 0x4342), off);
-            v0[2] = hsub2(__byte_perm(a23, ex, 0x4140), off);
-            v0[3] = hsub2(__byte_perm(a23, ex, 0x4342), off);
-            v1[0] = hsub2(__byte_perm(b01, ex, 0x4140), off);
-            v1[1] = hsub2(__byte_perm(b01, ex, 0x4342), off);
-            v1[2] = hsub2(__byte_perm(b23, ex, 0x4140), off);
-            v1[3] = hsub2(__byte_perm(b23, ex, 0x4342), off);
-          } else {
-            uint32_t x[4];
+          for (int i = 0; i < 4; ++i)
+            w[i] = *reinterpret_cast<const uint2*>(cv + gr * (64 * BITS) + (2 * j + ((i & 1) ^ swap) + 8 * (i >> 1)) * (4 * BITS) +
+                                                   r % LPG * 8);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              x[i] = *reinterpret_cast<const uint16_t*>(cv + c * 256 + (2 * j + (i & 1) + 8 * (i >> 1)) * 16 + r * 2);
-            const uint32_t w01 = __byte_perm(x[0], x[1], 0x5410), w23 = __byte_perm(x[2], x[3], 0x5410);
-            const uint32_t h01 = w01 >> 8, h23 = w23 >> 8;
-            constexpr uint32_t lm = 0x000F000Fu, hm = 0x00F000F0u, ex = 0x64006400u;
-            constexpr uint32_t off = 0x64086408u;                       // 1032
-            constexpr uint32_t s16 = 0x2C002C00u, o16 = 0xD480D480u;    // 1/16, -72
-            v0[0] = hsub2((w01 & lm) | ex, off);
-            v0[1] = hfma2((w01 & hm) | ex, s16, o16);
-            v0[2] = hsub2((w23 & lm) | ex, off);
-            v0[3] = hfma2((w23 & hm) | ex, s16, o16);
-            v1[0] = hsub2((h01 & lm) | ex, off);
-            v1[1] = hfma2((h01 & hm) | ex, s16, o16);
-            v1[2] = hsub2((h23 & lm) | ex, off);
-            v1[3] = hfma2((h23 & hm) | ex, s16, o16);
-          }
+          for (int h = 0; h < 16 / BITS; ++h) {   // four of the channels
+            auto word = [&](int i) { return (BITS == 8 ? h : h >> 1) ? w[i].y : w[i].x; };
+            uint32_t v0[4], v1[4];
+            if constexpr (BITS == 8) {
+              const uint32_t lo = swap ? 0x1504u : 0x5140u, hi = swap ? 0x3726u : 0x7362u;
+              const uint32_t a01 = __byte_perm(word(0), word(1), lo), b01 = __byte_perm(word(0), word(1), hi);
+              const uint32_t a23 = __byte_perm(word(2), word(3), lo), b23 = __byte_perm(word(2), word(3), hi);
+              constexpr uint32_t off = 0x64806480u, ex = 0x64646464u;   // 1152, 1152
+              v0[0] = hsub2(__byte_perm(a01, ex, 0x4140), off);
+              v0[1] = hsub2(__byte_perm(a01, ex, 0x4342), off);
+              v0[2] = hsub2(__byte_perm(a23, ex, 0x4140), off);
+              v0[3] = hsub2(__byte_perm(a23, ex, 0x4342), off);
+              v1[0] = hsub2(__byte_perm(b01, ex, 0x4140), off);
+              v1[1] = hsub2(__byte_perm(b01, ex, 0x4342), off);
+              v1[2] = hsub2(__byte_perm(b23, ex, 0x4140), off);
+              v1[3] = hsub2(__byte_perm(b23, ex, 0x4342), off);
+            } else {
+              const uint32_t sel = h & 1 ? (swap ? 0x3276u : 0x7632u) : (swap ? 0x1054u : 0x5410u);
+              const uint32_t w01 = __byte_perm(word(0), word(1), sel), w23 = __byte_perm(word(2), word(3), sel);
+              const uint32_t h01 = w01 >> 8, h23 = w23 >> 8;
+              constexpr uint32_t lm = 0x000F000Fu, hm = 0x00F000F0u, ex = 0x64006400u;
+              constexpr uint32_t off = 0x64086408u;                       // 1032
+              constexpr uint32_t s16 = 0x2C002C00u, o16 = 0xD480D480u;    // 1/16, -72
+              v0[0] = hsub2((w01 & lm) | ex, off);
+              v0[1] = hfma2((w01 & hm) | ex, s16, o16);
+              v0[2] = hsub2((w23 & lm) | ex, off);
+              v0[3] = hfma2((w23 & hm) | ex, s16, o16);
+              v1[0] = hsub2((h01 & lm) | ex, off);
+              v1[1] = hfma2((h01 & hm) | ex, s16, o16);
+              v1[2] = hsub2((h23 & lm) | ex, off);
+              v1[3] = hfma2((h23 & hm) | ex, s16, o16);
+            }
+            // the codes times their tokens' scales (registers 0, 1: tokens 2 j, 2 j + 1; 2, 3: and 8 on)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint32_t ps0 = hmul2(pb[n][0][0], sc0), ps1 = hmul2(pb[n][0][1], sc1);
-            mma_h(Y[n][2 * c], v0, ps0, ps1, Y[n][2 * c]);
-            mma_h(Y[n][2 * c + 1], v1, ps0, ps1, Y[n][2 * c + 1]);
+            for (int i = 0; i < 4; ++i) {
+              v0[i] = hmul2(v0[i], i < 2 ? sc0 : sc1);
+              v1[i] = hmul2(v1[i], i < 2 ? sc0 : sc1);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_h(Y[n][4 * c + 2 * h], v0, pb[n][0][0], pb[n][0][1], Y[n][4 * c + 2 * h]);
+              mma_h(Y[n][4 * c + 2 * h + 1], v1, pb[n][0][0], pb[n][0][1], Y[n][4 * c + 2 * h + 1]);
+            }
           }
         }
       }
@@ -694,10 +713,10 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
           a.w.pl[part * RB + q] = s;
         }
         if (rb * RB + q < R) {
-          float* y = a.w.pY + (part * RB + q) * 128 + 4 * r;
+          float* y = a.w.pY + (part * RB + q) * 128 + (BITS == 0 ? 4 * r : BITS == 8 ? 8 * r : 16 * r);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<float4*>(y + 32 * c) =
+            *reinterpret_cast<float4*>(y + (BITS == 0 ? 32 * c : BITS == 8 ? 64 * (c >> 1) + 4 * (c & 1) : 4 * c)) =
                 make_float4(Y[n][2 * c][e], Y[n][2 * c][2 + e], Y[n][2 * c + 1][e], Y[n][2 * c + 1][2 + e]);
         }
       }

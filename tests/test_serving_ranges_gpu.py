@@ -1,0 +1,156 @@
+"""The serving operators over their whole range: values at both ends of what the codes hold, blocks of three row tiles.
+
+Tolerances of bf16 layers (check_tree): 3e-3 in relative L2, 1e-2 of the largest output.  The output's rounding is 1.6e-3;
+q, a weight, a dequantised value (|error| <= 2^-11 of itself, and none for scales below the smallest normal fp16, whose
+products are multiples of 2^-24) and y are each rounded to fp16: below 4e-4 each.  Scaling all values by one number
+scales y and the output with it, so these bounds do not depend on it as long as y stays a normal fp16 number (6.1e-5 to
+65504); below that y is off by up to 2^-25, which the tests of small values add up themselves.
+"""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import serving_ref as R
+from test_serving_gpu import Plain, check_tree, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def put(c, b, K, V):
+    """Tokens K, V [n, hkv, d] (float64) at the end of sequence b, by the definition's packer."""
+    p, n = c.p, len(K)
+    t = torch.arange(len(c.K[b]), len(c.K[b]) + n)
+    R.put(c.pages, c.pt[b, t // 16], t % 16, K, V, p.bits, p.dt)
+    c.K[b] = torch.cat((c.K[b], R.stored(K, p.bits, p.dt)))
+    c.V[b] = torch.cat((c.V[b], R.stored(V.reshape(n, -1), p.bits, p.dt).reshape(n, p.hkv, p.d)))
+
+
+def seen(hist, n, sets):
+    see = torch.ones(n, hist + n, dtype=torch.bool)
+    for i in range(n):
+        for j in range(n):
+            see[i, hist + j] = j in sets[i] if sets is not None else j <= i
+    return see
+
+
+def tree(p, c, hist, counts, masks, q):
+    """One tree call of queries q [n, H, d] that need no rotation, and the definition: (out, want, call arguments)."""
+    off = np.cumsum([0] + counts).tolist()
+    want = []
+    for b, (h, k) in enumerate(zip(hist, counts)):
+        y = R.attention(q[off[b]:off[b + 1]], c.K[b], c.V[b], seen(h, k, masks[b] if masks else None), p.d ** -0.5)
+        want.append(y @ p.W_o)
+    words = max(1, -(-max(counts) // 32))
+    out = torch.full((off[-1], p.hidden), 9.0, dtype=p.dt, device="cuda")
+    ws = torch.empty(p.L.tree_workspace_bytes(len(hist), c.pt.shape[1] * 16, off[-1], max(counts)), dtype=torch.uint8,
+                     device="cuda").random_(0, 255)
+    args = dict(pool=c.upload(), n_pages=c.n_pages, page_table=c.pt_d, hist=i32(hist), node_off=i32(off), q=q.to(p.dt).cuda(),
+                out=out, workspace=ws, max_nodes=max(counts),
+                mask=R.mask_words(sum(masks, []), words).cuda() if masks else None)
+    p.L.tree_attn(**args)
+    return out.to(torch.float64).cpu(), torch.cat(want), args
+
+
+# rows per KV head: 1, 8, 16, 24 (blocks of 8, 16 and 24 rows), 32 (blocks of 128)
+ROWS = [(1, 1), (4, 2), (4, 4), (4, 6), (4, 8)]
+
+
+# ------------------------------------------------------------------ values at the ends of the codes' range
+
+@pytest.mark.parametrize("kind", ["random", "rising"])
+@pytest.mark.parametrize("group,n", ROWS)
+@pytest.mark.parametrize("bits", [8, 4])
+def test_tree_of_the_largest_values(bits, group, n, kind):
+    """Values up to 32000 (the codes hold 32768): every weight times its scale stays finite.  rising: scores that go up by
+    0.04 (log2) a token, so that the running maximum lags behind them."""
+    p = Plain(2 * group, 2, 128, bits, norm=False, rope=False)
+    hist, counts = [700, 333], [n, max(1, n - 1)]
+    c = p.cache([h + k for h, k in zip(hist, counts)])
+    g = torch.Generator().manual_seed(bits + n)
+    base = torch.where(torch.rand(128, generator=g) < 0.5, -1.0, 1.0).to(torch.float64)
+    q = p.r(torch.randn(sum(counts), p.H, 128, generator=g) * (0.3 if kind == "rising" else 1) + (base if kind == "rising" else 0))
+    for b in range(2):
+        T = hist[b] + counts[b]
+        K = torch.randn(T, 2, 128, generator=g, dtype=torch.float64)
+        if kind == "rising":
+            # a step of base * x in K moves a score by 128 x log2(e) / sqrt(128) = 16.3 x
+            K = 0.1 * K + base * (torch.arange(T) * (0.04 / 16.3))[:, None, None]
+        V = torch.randn(T, 2, 128, generator=g, dtype=torch.float64)
+        put(c, b, K, V * (32000.0 / V.abs().max()))
+    rng = random.Random(n)
+    for masks in ([R.random_tree(rng, k)[0] for k in counts], None):
+        got, want, _ = tree(p, c, hist, counts, masks, q)
+        check_tree(got, want, "bf16")
+    assert p.L.sync_status() == 0
+
+
+@pytest.mark.parametrize("H,hkv", [(2, 2), (8, 1), (16, 1), (24, 1), (40, 1)])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_decode_of_the_largest_values(bits, H, hkv):
+    p = Plain(H, hkv, 128, bits, norm=False)
+    lens = [1, 17, 900]
+    c = p.cache(lens)
+    g = torch.Generator().manual_seed(H)
+    for b, T in enumerate(lens):
+        K, V = (torch.randn(T, hkv, 128, generator=g, dtype=torch.float64) for _ in range(2))
+        put(c, b, K, V * (32000.0 / V.abs().max()))
+    q = p.r(torch.randn(3, H, 128, generator=g))
+    ws = torch.empty(p.L.workspace_bytes(3, c.pt.shape[1] * 16), dtype=torch.uint8, device="cuda").random_(0, 255)
+    out = torch.empty(3, p.hidden, dtype=p.dt, device="cuda")
+    p.L.decode(c.upload(), c.n_pages, c.pt_d, i32(lens), q.to(p.dt).cuda(), out, ws)
+    qx = p.norm_rope(q, None, torch.tensor(lens) - 1)
+    want = torch.cat([R.attention(qx[b:b + 1], c.K[b], c.V[b], torch.ones(1, T, dtype=torch.bool), 128 ** -0.5) @ p.W_o
+                      for b, T in enumerate(lens)])
+    check_tree(out.to(torch.float64).cpu(), want, "bf16")
+    assert p.L.sync_status() == 0
+
+
+@pytest.mark.parametrize("size,gap", [(1e-2, 15.5), (1e-3, 12.0)])
+@pytest.mark.parametrize("group,n", ROWS)
+@pytest.mark.parametrize("bits", [8, 4])
+def test_tree_of_small_values_beside_a_dominant_token(bits, group, n, size, gap):
+    """Every 128th token has nearly all of the weight and the value 0; the others, 2^-gap of its weight each, make up y:
+    about 127 2^-gap size = 2.7e-5 or 3.1e-5, whose fp16 rounding of at most 2^-25 is 1.1e-3 of it (7e-4 rms).
+
+    Blocks of 128 rows hold code * scale of the keys in fp16.  The dominant token's key has one magnitude in every
+    channel (base * gap / 16.3: one code and one scale), so its roundings, up to 2^-11 of the value, all have one sign and
+    move its score, gap above the others in log2 units, by up to gap * 2^-11: gap * ln 2 * 2^-11 of every other weight
+    (5.2e-3 and 4.1e-3), and of y.  Blocks of up to 24 rows score with the codes themselves."""
+    p = Plain(2 * group, 2, 128, bits, norm=False, rope=False)
+    hist, counts = [4096 - n, 4096 - n], [n, n]
+    c = p.cache([4096, 4096])
+    g = torch.Generator().manual_seed(n)
+    base = torch.where(torch.rand(128, generator=g) < 0.5, -1.0, 1.0).to(torch.float64)
+    q = p.r(torch.randn(2 * n, p.H, 128, generator=g) * 0.1 + base)
+    for b in range(2):
+        K = 0.3 * torch.randn(4096, 2, 128, generator=g, dtype=torch.float64)
+        V = size * (1 + 0.3 * torch.randn(4096, 2, 128, generator=g, dtype=torch.float64))
+        K[::128] = base * (gap / 16.3)
+        V[::128] = 0
+        put(c, b, K, V)
+    got, want, _ = tree(p, c, hist, counts, None, q)
+    key = gap * math.log(2) * 2.0 ** -11 if group * n >= 25 else 0.0
+    assert torch.linalg.norm(got - want) <= (3e-3 + key) * torch.linalg.norm(want)
+    assert (got - want).abs().max() <= (1e-2 + key) * want.abs().max()
+    assert p.L.sync_status() == 0
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("H,hkv,counts", [(8, 2, [5, 6, 4]), (2, 1, [12, 9, 0]), (6, 2, [8, 7, 6]), (24, 1, [1, 1, 1])])
+def test_tree_of_17_to_24_rows(bits, H, hkv, counts):
+    """Three tiles of 8 rows, full and not, with masks, over odd lengths."""
+    p = Plain(H, hkv, 128, bits, norm=False, rope=False)
+    hist = [515, 0, 33]
+    c = p.cache([h + k for h, k in zip(hist, counts)])
+    g = torch.Generator().manual_seed(H)
+    for b in range(3):
+        put(c, b, *(torch.randn(hist[b] + counts[b], hkv, 128, generator=g, dtype=torch.float64) for _ in range(2)))
+    rng = random.Random(H)
+    q = p.r(torch.randn(sum(counts), H, 128, generator=g))
+    for masks in ([R.random_tree(rng, k)[0] for k in counts], None):
+        got, want, _ = tree(p, c, hist, counts, masks, q)
+        check_tree(got, want, "bf16")
+    assert p.L.sync_status() == 0
