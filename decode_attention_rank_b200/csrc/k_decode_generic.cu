@@ -216,13 +216,13 @@ __global__ void k_value(LayerView v, const uint8_t* __restrict__ pool, long long
         float p = 0.f;
         if (t < ntk) {
           const float s = S[((size_t)row * v.H + hbase + h0 + k) * S_ld + tt + t];
-          p = s == -FLT_MAX ? 0.f : exp2f(s - m_s[k]);
+          p = s == -FLT_MAX ? -1.f : exp2f(s - m_s[k]);   // -1: a node that the row does not see
         }
         p_s[t][k] = p;
       }
       __syncthreads();
       if (threadIdx.x < nhc)
-        for (int t = 0; t < ntk; ++t) lsum += p_s[t][threadIdx.x];
+        for (int t = 0; t < ntk; ++t) lsum += p_s[t][threadIdx.x] < 0.f ? 0.f : p_s[t][threadIdx.x];
       if (cvalid) {
         for (int t = 0; t < ntk; ++t) {
           const int tok = tt + t;
@@ -232,8 +232,8 @@ __global__ void k_value(LayerView v, const uint8_t* __restrict__ pool, long long
             z = latent_value(v, pool + (size_t)page * v.page_bytes + ld.block_off, ld, tok % kPage, c);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            // a masked node's value is not read into the sum, whatever it holds
-            if (k < nhc && !(ri.row_hist && p_s[t][k] == 0.f)) acc[k] += p_s[t][k] * z;
+            // a masked node's value is not read into the sum, whatever it holds; a visible one is, whatever its weight (NaN passes)
+            if (k < nhc && !(p_s[t][k] < 0.f)) acc[k] += p_s[t][k] * z;
         }
       }
       __syncthreads();
@@ -258,15 +258,15 @@ __global__ void k_combine(LayerView v, RowInfo ri, int n_splits, const float* __
   float den = 0.f;
   for (int s = 0; s < n_splits; ++s) {
     const size_t i = ((size_t)row * n_splits + s) * v.H + h;
-    if (pl[i] > 0.f) den += exp2f(pm[i] - m) * pl[i];
+    if (pl[i] != 0.f) den += exp2f(pm[i] - m) * pl[i];   // (NaN passes)
   }
   for (int j = threadIdx.x; j < v.wv; j += blockDim.x) {
     float acc = 0.f;
     for (int s = 0; s < n_splits; ++s) {
       const size_t i = ((size_t)row * n_splits + s) * v.H + h;
-      if (pl[i] > 0.f) acc += exp2f(pm[i] - m) * pY[i * v.wv + j];
+      if (pl[i] != 0.f) acc += exp2f(pm[i] - m) * pY[i * v.wv + j];
     }
-    y[((size_t)row * v.H + h) * v.wv + j] = (TY)(den > 0.f ? acc / den : 0.f);
+    y[((size_t)row * v.H + h) * v.wv + j] = (TY)(den != 0.f ? acc / den : 0.f);
   }
 }
 
@@ -280,21 +280,21 @@ __global__ void k_combine_tiled(LayerView v, int n_splits, const float* __restri
   float den = 0.f;
   for (int s = 0; s < n_splits; ++s) {
     const size_t i = ((size_t)row * n_splits + s) * v.H + h;
-    if (pl[i] > 0.f) den += exp2f(pm[i] - m) * pl[i];
+    if (pl[i] != 0.f) den += exp2f(pm[i] - m) * pl[i];   // (NaN passes)
   }
   const int nt = row / NB, r = row % NB;
   for (int j = threadIdx.x; j < v.wv; j += blockDim.x) {
     float acc = 0.f;
     for (int s = 0; s < n_splits; ++s) {
       const size_t i = ((size_t)row * n_splits + s) * v.H + h;
-      if (pl[i] > 0.f) acc += exp2f(pm[i] - m) * pY[i * v.wv + j];
+      if (pl[i] != 0.f) acc += exp2f(pm[i] - m) * pY[i * v.wv + j];
     }
     const uint32_t k = (uint32_t)(h * v.wv + j);
     const uint32_t c = k & 63u;
     uint8_t* tile = ytiles + ((size_t)nt * KT + (k >> 6)) * (size_t)NB * 128;
     const uint32_t off = (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u + (((c >> 3) ^ (uint32_t)(r & 7)) << 4) +
                          (c & 7u) * 2u;
-    *reinterpret_cast<__half*>(tile + off) = __float2half_rn(den > 0.f ? acc / den : 0.f);
+    *reinterpret_cast<__half*>(tile + off) = __float2half_rn(den != 0.f ? acc / den : 0.f);
   }
 }
 

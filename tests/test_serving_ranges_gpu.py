@@ -1,4 +1,5 @@
-"""The serving operators over their whole range: values at both ends of what the codes hold, blocks of three row tiles.
+"""The serving operators over their whole range: values at both ends of what the codes hold, what a row sees of values
+that are not finite on every kernel, rows that see nothing, blocks of three row tiles.
 
 Tolerances of bf16 layers (check_tree): 3e-3 in relative L2, 1e-2 of the largest output.  The output's rounding is 1.6e-3;
 q, a weight, a dequantised value (|error| <= 2^-11 of itself, and none for scales below the smallest normal fp16, whose
@@ -14,6 +15,8 @@ import pytest
 import torch
 
 import serving_ref as R
+from harness import Case, GpuCache
+from synth import gen
 from test_serving_gpu import Plain, check_tree, i32
 
 pytestmark = pytest.mark.gpu
@@ -135,6 +138,131 @@ def test_tree_of_small_values_beside_a_dominant_token(bits, group, n, size, gap)
     key = gap * math.log(2) * 2.0 ** -11 if group * n >= 25 else 0.0
     assert torch.linalg.norm(got - want) <= (3e-3 + key) * torch.linalg.norm(want)
     assert (got - want).abs().max() <= (1e-2 + key) * want.abs().max()
+    assert p.L.sync_status() == 0
+
+
+# ------------------------------------------------------------------ values that are not finite, rows that see nothing
+
+# bf16 with head_dim 128 has kernels of its own (5 and 33 nodes of 4 heads a KV head: one of them each); the other layers
+# take the row kernels
+PLAIN = [("f32", 128, 2, 5), ("f32", 64, 2, 5), ("bf16", 64, 2, 5), ("bf16", 256, 1, 5), ("bf16", 80, 3, 5), ("bf16", 128, 1, 5),
+         ("bf16", 128, 4, 33)]
+
+
+def not_finite(call, plant, T, hist, sees):
+    """call() -> out after plant(token, side, value, low) wrote `value` into one channel of a token's key (side 0) or value
+    (side 1); low: its key makes the token's weight underflow.  Rows that see the token are infinite or NaN, the others
+    are as they were."""
+    clean = call()
+    assert torch.isfinite(clean).all()
+    n = len(sees)
+    for tok in (3, hist - 1, hist + 2):
+        rows = torch.tensor([tok < hist or tok - hist in s for s in sees])
+        assert rows.any()
+        for side, value, low in ((0, float("nan"), False), (1, float("nan"), False), (1, float("inf"), False),
+                                 (1, -float("inf"), False), (1, float("nan"), True)):
+            restore = plant(tok, side, value, low)
+            got = call()
+            restore()
+            bad = ~torch.isfinite(got).all(1)
+            assert torch.equal(bad, rows), (tok, side, value, low)
+            assert torch.equal(got[~rows], clean[~rows])
+    assert torch.equal(call(), clean)
+
+
+@pytest.mark.parametrize("dtype,d,group,n", PLAIN)
+def test_tree_rows_that_see_a_value_that_is_not_finite(dtype, d, group, n):
+    """Over 1300 tokens: the row kernels split them, and the other splits are finite."""
+    hkv, hist = 2, 1300
+    p = Plain(hkv * group, hkv, d, 0, dtype, norm=False, rope=False)
+    c = p.cache([hist + n])
+    g = torch.Generator().manual_seed(d)
+    base = torch.where(torch.rand(d, generator=g) < 0.5, -1.0, 1.0).to(torch.float64)
+    q = p.r(0.3 * torch.randn(n, p.H, d, generator=g) + base)
+    K, V = (torch.randn(hist + n, hkv, d, generator=g, dtype=torch.float64) for _ in range(2))
+    put(c, 0, K, V)
+    rng = random.Random(d)
+    sees = R.random_tree(rng, n)[0]
+    sees[1], sees[2], sees[3] = {0, 1}, {0, 2}, {1, 3}
+    _, want, args = tree(p, c, [hist], [n], [sees], q)
+
+    def call():
+        p.L.tree_attn(**dict(args, pool=c.upload()))
+        return args["out"].to(torch.float64).cpu()
+
+    def plant(tok, side, value, low):
+        k, v = c.K[0][tok:tok + 1].clone(), c.V[0][tok:tok + 1].clone()
+        if low:   # a score of -1.44 d 300 / (16 sqrt(d)) = -27 sqrt(d) or less: its weight is below the smallest fp32
+            k = (-300.0 / 16 * base).expand_as(k).clone()
+        (v if side else k)[0, :, d // 2] = value
+        at = c.pt[0, tok // 16:tok // 16 + 1], torch.tensor([tok % 16])
+        before = c.pages.clone()
+        R.put(c.pages, *at, k, v, 0, p.dt)
+
+        def restore():
+            c.pages.copy_(before)
+        return restore
+
+    check_tree(call(), want, dtype)
+    not_finite(call, plant, hist + n, hist, sees)
+    assert p.L.sync_status() == 0
+
+
+@pytest.mark.parametrize("cfg", [1, 3])
+def test_tree_of_a_latent_layer_and_values_that_are_not_finite(cfg):
+    spec = gen.config_spec(cfg, quantized=False)
+    case = Case(spec, 11)
+    L = case.load()
+    hist, n = 1100, 5
+    Z = case.latents_direct(0, hist + n)
+    sees = [{0}, {0, 1}, {0, 2}, {1, 3}, {0, 2, 4}]
+    cache = GpuCache(L, [hist + n])
+    cache.append_latents(0, Z)
+    g = torch.Generator().manual_seed(2)
+    q = (torch.randn(n, spec.n_heads, spec.head_dim, generator=g) / spec.head_dim ** 0.5 * 3).to(torch.bfloat16).cuda()
+    out = torch.empty(n, spec.hidden, dtype=torch.bfloat16, device="cuda")
+    mp = cache.page_table.shape[1]
+    ws = torch.empty(L.tree_workspace_bytes(1, mp * 16, n, n), dtype=torch.uint8, device="cuda")
+
+    def call():
+        L.tree_attn(cache.pool, cache.n_pages, cache.page_table[:1], i32([hist]), i32([0, n]), q, out, ws, max_nodes=n,
+                    mask=R.mask_words(sees, 1).cuda(), q_pos=i32(range(hist, hist + n)))
+        return out.to(torch.float64).cpu()
+
+    def write(z, tok):
+        # clear the slot (a path of no nodes), then write it again
+        L.tree_accept(cache.pool, cache.n_pages, cache.page_table[:1], i32([tok]), i32([0, 1]), i32([0]), i32([0]), max_nodes=1)
+        cache.append_latents(0, z, start=tok)
+
+    clean = call()
+    assert torch.isfinite(clean).all()
+    for tok in (3, hist - 1, hist + 2):
+        rows = torch.tensor([tok < hist or tok - hist in s for s in sees])
+        for side, value in ((0, float("nan")), (1, float("nan")), (1, float("inf"))):
+            z = [x[tok:tok + 1].copy() for x in Z]
+            for x in (z[-1:] if side else z[:-1]):
+                x[0, 1] = value
+            write(z, tok)
+            got = call()
+            write([x[tok:tok + 1] for x in Z], tok)
+            assert torch.equal(~torch.isfinite(got).all(1), rows), (tok, side, value)
+            assert torch.equal(got[~rows], clean[~rows])
+    assert torch.equal(call(), clean)
+    assert L.sync_status() == 0
+
+
+@pytest.mark.parametrize("dtype,d,bits", [("f32", 128, 0), ("bf16", 64, 8), ("bf16", 256, 4), ("bf16", 80, 0), ("bf16", 128, 4)])
+def test_tree_rows_that_see_nothing_on_every_kernel(dtype, d, bits):
+    p = Plain(4, 2, d, bits, dtype)
+    hist, counts = [0, 0, 20], [3, 2, 2]
+    masks = [[set(), {1}, {0, 2}], [set(), set()], [{0}, set()]]
+    c = p.cache([h + k for h, k in zip(hist, counts)])
+    g = torch.Generator().manual_seed(d)
+    for b in range(3):
+        put(c, b, *(torch.randn(hist[b] + counts[b], 2, d, generator=g, dtype=torch.float64) for _ in range(2)))
+    got, want, _ = tree(p, c, hist, counts, masks, p.r(torch.randn(7, 4, d, generator=g)))
+    assert torch.all(got[0] == 0) and torch.all(got[3:5] == 0)
+    check_tree(got, want, dtype)
     assert p.L.sync_status() == 0
 
 
