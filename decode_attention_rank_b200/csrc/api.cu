@@ -144,7 +144,7 @@ static starkv_status plan_layer(starkv_layer* L, int kv_bits) {
   }
   L->page_bytes = ru(off, 128);
   L->bytes_per_token = bpt;
-  LayerView& v = L->view;
+  ServeView& v = L->view;
   v.D = c.hidden;
   v.H = c.n_heads;
   v.Hkv = Hkv;
@@ -282,7 +282,7 @@ static starkv_status load_layer(const starkv_layer_config* cfg, const PlainOpts*
   L->cfg.key_ranks = nullptr;
   cudaGetDevice(&L->device);
   plan_layer(L, opts ? opts->kv_bits : 0);
-  LayerView& v = L->view;
+  ServeView& v = L->view;
   const int D = v.D, d = v.d, H = v.H;
   const size_t es = cfg->dtype == STARKV_F32 ? 4 : 2;
   auto fail = [&](starkv_status code, const char* what) {

@@ -63,7 +63,7 @@ starkv_status starkv_qk_norm_rope(const starkv_layer* L, int n_tokens, const int
   CHECK_ARG(aligned_to(q, 4) && aligned_to(k, 4) && aligned_to(q_out, 4) && aligned_to(k_out, 4) && q_ld >= 0 &&
                 k_ld >= 0 && q_out_ld >= 0 && k_out_ld >= 0,
             "rows must be 4-byte aligned and their strides non-negative");
-  const LayerView& v = L->view;
+  const ServeView& v = L->view;
   if (!v.opt) {
     set_error("only layers of starkv_load_plain");
     return STARKV_ERR_UNSUPPORTED;
@@ -110,7 +110,7 @@ starkv_status starkv_append_qkv(const starkv_layer* L, void* pool, int64_t n_pag
   CHECK_ARG(aligned_to(q, 4) && aligned_to(k, 4) && aligned_to(vv, 4) && aligned_to(q_out, 4) && q_ld >= 0 &&
                 k_ld >= 0 && v_ld >= 0 && q_out_ld >= 0,
             "rows must be 4-byte aligned and their strides non-negative");
-  const LayerView& v = L->view;
+  const ServeView& v = L->view;
   if (!v.opt) {
     set_error("only layers of starkv_load_plain");
     return STARKV_ERR_UNSUPPORTED;
@@ -200,7 +200,7 @@ starkv_status starkv_tree_attn(const starkv_layer* L, const void* pool, int64_t 
                 aligned_to(q_pos, 4),
             "page_table, hist, node_off, mask and q_pos must be 4-byte aligned");
   CHECK_LAYER(L);
-  const LayerView& v = L->view;
+  const ServeView& v = L->view;
   CHECK_ARG(q_pos || v.plain || !v.rope, "a latent layer with RoPE needs q_pos");
   const size_t need = starkv_tree_workspace_bytes(L, batch, max_pages * kPage, n_nodes, max_nodes);
   if (workspace == nullptr || ws_bytes < need) {

@@ -143,7 +143,8 @@ __global__ void k_pack(LayerView v, uint8_t* __restrict__ pool, long long n_page
 }
 
 // Quantized latents: one warp per (token, group) so that no warp walks a
-// latent's groups one after another.
+// latent's groups one after another.  KV: codes of an uncompressed layer.
+template <bool KV>
 __global__ void k_pack_groups(LayerView v, const int* __restrict__ grp_lat, int n_grp, uint8_t* __restrict__ pool,
                               long long n_pages, const int32_t* __restrict__ pt, int n_seqs, int max_pages, int n,
                               const int32_t* __restrict__ seq_idx, const int32_t* __restrict__ pos,
@@ -174,10 +175,10 @@ __global__ void k_pack_groups(LayerView v, const int* __restrict__ grp_lat, int 
   float amax = lane < gd.n ? fabsf(x) : 0.f;
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const int qmax = (1 << (gd.bits - 1)) - 1;
-  // uncompressed layers' codes (kv_bits): the scale of starkv_append_qkv, a product with the rounded 1 / qmax, and a
+  // uncompressed layers' codes: the scale of starkv_append_qkv, a product with the rounded 1 / qmax, and a
   // group that has no code stored as zeros
-  float s32 = v.kv_bits ? __fmul_rn(amax, __fdiv_rn(1.f, (float)qmax)) : __fdiv_rn(amax, (float)qmax);
-  if (v.kv_bits) {
+  float s32 = KV ? __fmul_rn(amax, __fdiv_rn(1.f, (float)qmax)) : __fdiv_rn(amax, (float)qmax);
+  if (KV) {
     const bool bad = __any_sync(0xffffffffu, !(fabsf(x) <= kKvMax));
     if (bad) {
       if (lane == 0) atomicOr(v.status, kScaleOvf);
@@ -212,7 +213,7 @@ cudaError_t launch_pack(const starkv_layer* L, uint8_t* pool, long long n_pages,
   if (v.quantized && L->d_grp_lat) {
     const int ng = (int)L->grp.size();
     const long long warps = (long long)n * ng;
-    k_pack_groups<<<(unsigned)((warps * 32 + threads - 1) / threads), threads, 0, s>>>(
+    (L->view.kv_bits ? k_pack_groups<true> : k_pack_groups<false>)<<<(unsigned)((warps * 32 + threads - 1) / threads), threads, 0, s>>>(
         v, L->d_grp_lat, ng, pool, n_pages, page_table, n_seqs, max_pages, n, seq_idx, positions, z, rotate);
     return cudaGetLastError();
   }

@@ -14,6 +14,8 @@
 //   out     out = sum_h y_h M_h with the fused factors (steps 7-8)
 #include <float.h>
 
+#include <type_traits>
+
 #include "starkv_internal.cuh"
 
 namespace starkv {
@@ -51,46 +53,58 @@ __device__ __forceinline__ float ldf<__nv_bfloat16>(const __nv_bfloat16* p, size
   return __bfloat162float(p[i]);
 }
 
-// qrot[row][h][p] = RoPE(q, pos)[p] * scale * log2(e)
-template <typename T>
-__global__ void k_qprep(LayerView v, const T* __restrict__ q, RowInfo ri, float* __restrict__ qrot) {
+// Rows R: RowInfo, or TreeRows for the nodes of drafted trees.
+template <typename R>
+constexpr bool kTree = std::is_same_v<R, TreeRows>;
+
+// qrot[row][h][p] = RoPE(q, pos)[p] * scale * log2(e); V = ServeView: layers of starkv_load_plain, and nodes
+template <typename T, typename V, typename R>
+__global__ void k_qprep(V v, const T* __restrict__ q, R ri, float* __restrict__ qrot) {
+  constexpr bool kServe = std::is_same_v<V, ServeView>;
   const int row = blockIdx.x, h = blockIdx.y, d = v.d, half = d / 2;
   const T* qh = q + ((size_t)row * v.H + h) * d;
   float* o = qrot + ((size_t)row * v.H + h) * d;
-  if (ri.row_hist && !ri.node_pos) {   // queries are normed and rotated already
-    for (int p = threadIdx.x; p < d; p += blockDim.x) o[p] = ldf(qh, p) * v.scale_log2;
-    return;
+  if constexpr (kTree<R>) {
+    if (!ri.node_pos) {   // queries are normed and rotated already
+      for (int p = threadIdx.x; p < d; p += blockDim.x) o[p] = ldf(qh, p) * v.scale_log2;
+      return;
+    }
   }
   const int pos = row_pos_of(ri, row);
+  const float* w = nullptr;   // norm weights
   float inv = 1.f;
-  if (v.q_norm) {
-    __shared__ float red[2];
-    float s = 0.f;
-    for (int p = threadIdx.x; p < d; p += blockDim.x) {
-      const float x = ldf(qh, p);
-      s += x * x;
+  if constexpr (kServe) {
+    w = v.q_norm;
+    if (w) {
+      __shared__ float red[2];
+      float s = 0.f;
+      for (int p = threadIdx.x; p < d; p += blockDim.x) {
+        const float x = ldf(qh, p);
+        s += x * x;
+      }
+      for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+      __syncthreads();
+      inv = 1.f / sqrtf((red[0] + red[1]) / (float)d + v.norm_eps);
     }
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    inv = 1.f / sqrtf((red[0] + red[1]) / (float)d + v.norm_eps);
   }
   for (int p = threadIdx.x; p < half; p += blockDim.x) {
     float a = ldf(qh, p), b = ldf(qh, p + half);
-    if (v.q_norm) {
-      a *= inv * v.q_norm[p];
-      b *= inv * v.q_norm[p + half];
+    if (w) {
+      a *= inv * w[p];
+      b *= inv * w[p + half];
     }
-    if (v.rope && v.opt) {
+    if (v.rope) {
       double sn, cs;
-      const double t = (double)pos * v.turn[p];
-      sincospi(2.0 * (t - rint(t)), &sn, &cs);
-      const float a2 = (float)(a * cs - b * sn), b2 = (float)(b * cs + a * sn);
-      a = a2;
-      b = b2;
-    } else if (v.rope) {
-      double sn, cs;
-      sincos((double)pos * rope_freq(p, d, v.rope_log2_theta), &sn, &cs);
+      bool turns = false;
+      if constexpr (kServe) {
+        turns = v.opt;
+        if (turns) {
+          const double t = (double)pos * v.turn[p];
+          sincospi(2.0 * (t - rint(t)), &sn, &cs);
+        }
+      }
+      if (!turns) sincos((double)pos * rope_freq(p, d, v.rope_log2_theta), &sn, &cs);
       const float a2 = (float)(a * cs - b * sn), b2 = (float)(b * cs + a * sn);
       a = a2;
       b = b2;
@@ -101,8 +115,9 @@ __global__ void k_qprep(LayerView v, const T* __restrict__ q, RowInfo ri, float*
 }
 
 // Scores (log2 units) S[row][h][t] for one KV head and one 64-token tile.
+template <typename R>
 __global__ void k_scores(LayerView v, const uint8_t* __restrict__ pool, long long n_pages,
-                         const int32_t* __restrict__ pt, int max_pages, RowInfo ri, const float* __restrict__ Bk,
+                         const int32_t* __restrict__ pt, int max_pages, R ri, const float* __restrict__ Bk,
                          const int* __restrict__ key_off, const float* __restrict__ qrot, float* __restrict__ S,
                          int S_ld) {
   extern __shared__ float smem[];
@@ -141,8 +156,11 @@ __global__ void k_scores(LayerView v, const uint8_t* __restrict__ pool, long lon
       for (int idx = threadIdx.x; idx < nt * half; idx += blockDim.x) {
         const int t = idx / half, p = idx % half;
         // a drafted node's key stands at the node's position, not at its slot
-        const int hist = ri.row_hist ? ri.row_hist[row] : 0;
-        const int kpos = ri.node_pos && t0 + t >= hist ? ri.node_pos[ri.node_off[b] + (t0 + t - hist)] : t0 + t;
+        int kpos = t0 + t;
+        if constexpr (kTree<R>) {
+          const int j = kpos - ri.row_hist[row];
+          if (ri.node_pos && j >= 0) kpos = ri.node_pos[ri.node_off[b] + j];
+        }
         double sn, cs;
         sincos((double)kpos * rope_freq(p, d, v.rope_log2_theta), &sn, &cs);
         const float a = Kt[t * d + p], bb = Kt[t * d + p + half];
@@ -157,7 +175,7 @@ __global__ void k_scores(LayerView v, const uint8_t* __restrict__ pool, long lon
     const float* qh = qrot + ((size_t)row * v.H + h) * d;
     float acc = 0.f;
     for (int p = 0; p < d; ++p) acc += qh[p] * Kt[t * d + p];
-    if (ri.row_hist) {
+    if constexpr (kTree<R>) {
       const int j = t0 + t - ri.row_hist[row];
       if (j >= 0 && !tree_sees(ri.mask, ri.mask_words, row, ri.row_node[row], j)) acc = -FLT_MAX;
     }
@@ -168,9 +186,12 @@ __global__ void k_scores(LayerView v, const uint8_t* __restrict__ pool, long lon
 // Value partials for one (row, split, block of value channels).  Joint
 // latents: every query head reads every channel (stacked-head contraction on
 // the shared latent).  Plain layers: a block lies inside one KV head's d
-// channels and serves that head's query group.
+// channels and serves that head's query group.  Nodes have the tokens that
+// they do not see at -FLT_MAX in every head; those are left out, whatever their values hold.  (A test in every product,
+// for decodes and prefills too, made a decode of 4 x 1000 tokens 1.3 to 2.3 times as long.)
+template <typename R>
 __global__ void k_value(LayerView v, const uint8_t* __restrict__ pool, long long n_pages,
-                        const int32_t* __restrict__ pt, int max_pages, RowInfo ri, const float* __restrict__ S,
+                        const int32_t* __restrict__ pt, int max_pages, R ri, const float* __restrict__ S,
                         int S_ld, int n_splits, int chunk, int vb, float* __restrict__ pY, float* __restrict__ pm,
                         float* __restrict__ pl) {
   __shared__ float m_s[32];
@@ -214,17 +235,22 @@ __global__ void k_value(LayerView v, const uint8_t* __restrict__ pool, long long
       for (int idx = threadIdx.x; idx < 32 * nhc; idx += blockDim.x) {
         const int t = idx % 32, k = idx / 32;
         float p = 0.f;
-        if (t < ntk) {
-          const float s = S[((size_t)row * v.H + hbase + h0 + k) * S_ld + tt + t];
-          p = s == -FLT_MAX ? -1.f : exp2f(s - m_s[k]);   // -1: a node that the row does not see
+        if constexpr (kTree<R>) {
+          if (t < ntk) {
+            const float s = S[((size_t)row * v.H + hbase + h0 + k) * S_ld + tt + t];
+            p = s == -FLT_MAX ? -1.f : exp2f(s - m_s[k]);   // -1: a node that the row does not see
+          }
+        } else if (t < ntk) {
+          p = exp2f(S[((size_t)row * v.H + hbase + h0 + k) * S_ld + tt + t] - m_s[k]);
         }
         p_s[t][k] = p;
       }
       __syncthreads();
       if (threadIdx.x < nhc)
-        for (int t = 0; t < ntk; ++t) lsum += p_s[t][threadIdx.x] < 0.f ? 0.f : p_s[t][threadIdx.x];
+        for (int t = 0; t < ntk; ++t) lsum += kTree<R> && p_s[t][threadIdx.x] < 0.f ? 0.f : p_s[t][threadIdx.x];
       if (cvalid) {
         for (int t = 0; t < ntk; ++t) {
+          if (kTree<R> && p_s[t][0] < 0.f) continue;   // (a visible value counts whatever its weight: 0 times NaN is NaN)
           const int tok = tt + t;
           const int page = pt[(size_t)b * max_pages + tok / kPage];
           float z = 0.f;
@@ -232,8 +258,7 @@ __global__ void k_value(LayerView v, const uint8_t* __restrict__ pool, long long
             z = latent_value(v, pool + (size_t)page * v.page_bytes + ld.block_off, ld, tok % kPage, c);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            // a masked node's value is not read into the sum, whatever it holds; a visible one is, whatever its weight (NaN passes)
-            if (k < nhc && !(p_s[t][k] < 0.f)) acc[k] += p_s[t][k] * z;
+            if (k < nhc) acc[k] += p_s[t][k] * z;
         }
       }
       __syncthreads();
@@ -376,36 +401,37 @@ WsPlan plan_ws(const starkv_layer* L, int rows, int max_len, bool prefill) {
   return p;
 }
 
-}  // namespace
-
-size_t decode_generic_ws_bytes(const starkv_layer* L, int rows, int max_len, bool prefill) {
-  return plan_ws(L, rows, max_len, prefill).total;
-}
-
-cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, long long n_pages,
-                                  const int32_t* page_table, int max_pages, int rows, RowInfo ri, int max_len,
-                                  const void* q, void* out, void* ws, size_t ws_bytes, bool prefill,
-                                  cudaStream_t s, bool tc_scores) {
+// The row kernels up to the merge.
+template <typename R>
+cudaError_t launch_rows(const starkv_layer* L, const uint8_t* pool, long long n_pages, const int32_t* page_table,
+                               int max_pages, int rows, const R& ri, int max_len, const void* q, const WsPlan& p, char* w,
+                               cudaStream_t s, bool tc_scores) {
   const LayerView& v = L->view;
-  const WsPlan p = plan_ws(L, rows, max_len, prefill);
-  if (ws_bytes < p.total) return cudaErrorInvalidValue;
-  char* w = (char*)ws;
   float* qrot = (float*)(w + p.qrot);
   float* S = (float*)(w + p.S);
   float* pm = (float*)(w + p.pm);
   float* pl = (float*)(w + p.pl);
   float* pY = (float*)(w + p.pY);
-  void* y = w + p.y;
-  if (v.dtype == STARKV_F32)
-    k_qprep<float><<<dim3(rows, v.H), 64, 0, s>>>(v, (const float*)q, ri, qrot);
+  const dim3 qgrid(rows, v.H);
+  auto qprep = [&](const auto& view) {
+    using V = std::decay_t<decltype(view)>;
+    if (v.dtype == STARKV_F32)
+      k_qprep<float, V, R><<<qgrid, 64, 0, s>>>(view, (const float*)q, ri, qrot);
+    else
+      k_qprep<__nv_bfloat16, V, R><<<qgrid, 64, 0, s>>>(view, (const __nv_bfloat16*)q, ri, qrot);
+  };
+  if constexpr (kTree<R>)
+    qprep(L->view);
+  else if (L->view.opt)
+    qprep(L->view);
   else
-    k_qprep<__nv_bfloat16><<<dim3(rows, v.H), 64, 0, s>>>(v, (const __nv_bfloat16*)q, ri, qrot);
+    qprep(v);
   int rmax = 0;
   for (int g = 0; g < v.Hkv; ++g) rmax = std::max(rmax, L->lat[g].width);
   const size_t smem = sizeof(float) * kTile * (size_t)(rmax + v.d);
-  cudaError_t e = set_smem_limit((const void*)k_scores, smem);
+  cudaError_t e = set_smem_limit((const void*)k_scores<R>, smem);
   if (e != cudaSuccess) return e;
-  const bool plain = plain_decode_supported(v) && !tc_scores && !ri.row_hist;
+  const bool plain = plain_decode_supported(v) && !tc_scores && !kTree<R>;
   if (plain) {
     // uncompressed bf16 layer: one streaming pass over K and V, partials for the merge below
     e = launch_plain_decode(L, pool, n_pages, page_table, max_pages, rows, ri, qrot, p.n_splits, p.chunk, pY, pm, pl,
@@ -418,19 +444,44 @@ cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, lo
                          S, p.S_ld, s);
     if (e != cudaSuccess) return e;
   } else {
-    k_scores<<<dim3((max_len + kTile - 1) / kTile, v.Hkv, rows), 256, smem, s>>>(
+    k_scores<R><<<dim3((max_len + kTile - 1) / kTile, v.Hkv, rows), 256, smem, s>>>(
         v, pool, n_pages, page_table, max_pages, ri, L->Bk, L->d_key_off, qrot, S, p.S_ld);
   }
   if (!plain) {
     const int vb = value_block(v);
     const int cblocks = (v.rv + vb - 1) / vb;
-    k_value<<<dim3(cblocks, p.n_splits, rows), kVBlock, 0, s>>>(v, pool, n_pages, page_table, max_pages, ri, S,
-                                                                p.S_ld, p.n_splits, p.chunk, vb, pY, pm, pl);
+    k_value<R><<<dim3(cblocks, p.n_splits, rows), kVBlock, 0, s>>>(v, pool, n_pages, page_table, max_pages, ri, S, p.S_ld,
+                                                                   p.n_splits, p.chunk, vb, pY, pm, pl);
   }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_generic_ws_bytes(const starkv_layer* L, int rows, int max_len, bool prefill) {
+  return plan_ws(L, rows, max_len, prefill).total;
+}
+
+cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, long long n_pages,
+                                  const int32_t* page_table, int max_pages, int rows, RowInfo ri, int max_len,
+                                  const void* q, void* out, void* ws, size_t ws_bytes, bool prefill,
+                                  cudaStream_t s, bool tc_scores, const TreeRows* tree) {
+  const LayerView& v = L->view;
+  const WsPlan p = plan_ws(L, rows, max_len, prefill);
+  if (ws_bytes < p.total) return cudaErrorInvalidValue;
+  char* w = (char*)ws;
+  float* pm = (float*)(w + p.pm);
+  float* pl = (float*)(w + p.pl);
+  float* pY = (float*)(w + p.pY);
+  void* y = w + p.y;
+  const int32_t* n_rows = tree ? tree->n_rows : nullptr;
+  cudaError_t e = tree ? launch_rows(L, pool, n_pages, page_table, max_pages, rows, *tree, max_len, q, p, w, s, tc_scores)
+                       : launch_rows(L, pool, n_pages, page_table, max_pages, rows, ri, max_len, q, p, w, s, tc_scores);
+  if (e != cudaSuccess) return e;
   if (v.dtype == STARKV_F32) {
     k_combine<float><<<dim3(rows, v.H), 128, 0, s>>>(v, ri, p.n_splits, pY, pm, pl, (float*)y);
     k_out<float, float><<<(v.D * 32 + 255) / 256, 256, 0, s>>>((const float*)y, (const float*)L->M_T, rows,
-                                                                v.H * v.wv, v.D, ri.n_rows, (float*)out);
+                                                                v.H * v.wv, v.D, n_rows, (float*)out);
     return cudaGetLastError();
   }
   const int NB = outproj_nb(rows);
@@ -443,7 +494,7 @@ cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, lo
   k_combine_tiled<<<dim3(rows, v.H), 128, 0, s>>>(v, p.n_splits, pY, pm, pl, NB, KT, (uint8_t*)y);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_outproj_tc(L, y, rows, out, (float*)(w + p.part), s, ri.n_rows);
+  return launch_outproj_tc(L, y, rows, out, (float*)(w + p.part), s, n_rows);
 }
 
 namespace {
@@ -504,7 +555,7 @@ cudaError_t launch_tree_generic(const starkv_layer* L, const TreeArgs& t, void* 
   cudaError_t e = cudaGetLastError();
   const size_t es = L->view.dtype == STARKV_F32 ? 4 : 2;
   for (int r0 = 0; r0 < n && e == cudaSuccess; r0 += kTreeRows) {
-    RowInfo ri{tab + r0, tab + n + r0, tab + 2 * n + r0};
+    TreeRows ri{{tab + r0, tab + n + r0, tab + 2 * n + r0}};
     ri.row_hist = tab + 3 * n + r0;
     ri.row_node = tab + 4 * n + r0;
     ri.n_rows = tab + 5 * n + r0 / kTreeRows;
@@ -515,7 +566,7 @@ cudaError_t launch_tree_generic(const starkv_layer* L, const TreeArgs& t, void* 
     e = launch_decode_generic(L, t.pool, t.n_pages, t.pt, t.max_pages, std::min(kTreeRows, n - r0), ri, max_len,
                               (const char*)t.q + (size_t)r0 * L->view.H * L->view.d * es,
                               (char*)t.out + (size_t)r0 * L->view.D * es, (char*)ws + tab_bytes, ws_bytes - tab_bytes,
-                              false, s);
+                              false, s, false, &ri);
   }
   return e;
 }

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
   constexpr int V = Vec<T>::N, HALF = D / 2, LPR = HALF / V, RPW = 32 / LPR;
   __shared__ double2 cs_d[BITS ? HALF : 1];
   __shared__ __align__(16) float cs_c[HALF], cs_s[HALF];
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x, nw = blockDim.x >> 5, b0 = blockIdx.y * nw * per, b1 = min(groups, b0 + nw * per);
   const int nq = a.q ? (v.H + RPW - 1) / RPW : 0, nk = a.k ? (v.Hkv + RPW - 1) / RPW : 0;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int
 // Any even head_dim up to 256, unquantised pages: one warp per row, a lane per pair.
 template <typename T>
 __global__ void __launch_bounds__(kKvThreads) k_qkv_any(KvArgs a) {
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const int half = v.d / 2, lane = threadIdx.x & 31;
   const int nq = a.q ? v.H : 0, nk = a.k ? v.Hkv : 0, nv = a.vv ? v.Hkv : 0, rows = nq + nk + nv;
   const long long w = ((long long)blockIdx.x * kKvThreads + threadIdx.x) >> 5;
@@ -503,7 +503,7 @@ constexpr int kReadUnroll = 4;
 
 template <typename TO, int BITS, int CPH>   // BITS 0: stored in the layer dtype TO
 __global__ void __launch_bounds__(32 * kReadWarps) k_read8(KvArgs a, int chunks_per_warp, TO* __restrict__ out) {
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const int lane = threadIdx.x & 31;
   const long long i = (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
   if (i >= a.n) return;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) k_read8(KvArgs a, int chunks_
 
 template <typename TO>
 __global__ void __launch_bounds__(256) k_read_any(KvArgs a, TO* __restrict__ out) {
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const long long w = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;   // a warp per (token, latent)
   if (w >= (long long)a.n * v.L) return;
   const int i = (int)(w / v.L), li = (int)(w % v.L), lane = threadIdx.x & 31;
@@ -872,7 +872,7 @@ cudaError_t read_plain(const KvArgs& a, void* out, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_cache_read(const KvArgs& a, void* out, cudaStream_t s) {
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const bool f32 = v.dtype == STARKV_F32;
   // eight channels a lane: rows of whole 8-channel chunks
   if (v.plain && v.d % 8 == 0) {
@@ -894,7 +894,7 @@ cudaError_t launch_accept(const starkv_layer* L, uint8_t* pool, long long n_page
                           const int32_t* acc, const int32_t* n_acc, cudaStream_t s) {
   AcceptArgs a{L->view, pool, n_pages, pt, max_pages, batch, n_nodes, max_nodes, hist, node_off, acc, n_acc,
                L->d_grp_lat, (int)L->grp.size()};
-  const LayerView& v = L->view;
+  const ServeView& v = L->view;
   const int slot_bytes = v.kv_bits ? 2 * v.Hkv * v.d * v.kv_bits / 8 : 2 * v.Hkv * v.d * v.es;
   if (v.plain && (v.d * v.es) % 16 == 0) {
     const int pieces = slot_bytes / 16;

@@ -35,6 +35,7 @@ struct OutArgs {
   int stages;
   uint32_t tmem_cols;
   uint32_t* status;
+  int early;          // launched early: M's first tiles are asked for before the wait
 };
 
 __device__ __forceinline__ long long unit_begin(int c, int G, long long U) { return (long long)c * U / G; }
@@ -75,8 +76,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) k_outproj_tc(OutArgs a) {
 
   if (warp == 0) {
     if (lane == 0) {
-      // M does not depend on the kernels before: the first stages' tiles are on their way while those still run
-      const int ahead = (int)min((long long)a.stages, u1 - u0);
+      // M does not depend on the kernels before: the first stages' tiles are on their way while those still run.  (Nothing does in
+      // other launches, where the wait for all of them before the first of y took 1 us longer.)
+      const int ahead = a.early ? (int)min((long long)a.stages, u1 - u0) : 0;
       for (int i = 0; i < ahead; ++i) {
         tc::mbar_expect_tx(&full[i], a_bytes + b_bytes);
         tc::bulk_g2s(A_s + (size_t)i * a_bytes, a.M + ((size_t)u0 + i) * a_bytes, a_bytes, &full[i]);
@@ -307,6 +309,7 @@ cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, con
   while (cols < (uint32_t)(2 * NB)) cols <<= 1;
   a.tmem_cols = cols;
   a.status = status;
+  a.early = early;
   const size_t smem = (size_t)a.stages * stage_bytes + 1024;
   cudaError_t e = set_smem_limit((const void*)k_outproj_tc, smem);
   if (e != cudaSuccess) return e;

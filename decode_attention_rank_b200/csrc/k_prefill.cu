@@ -27,6 +27,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "tc_common.cuh"
 
 namespace starkv {
@@ -52,22 +54,21 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 // cos / sin of every (query, pair) of the chunk, shared by all heads: query i
 // (position q_start + i), pair p: the angle reduced modulo 2 pi in double,
 // then a float sincos.  cs[i][p] = (cos, sin).
-__global__ void k_prefill_qrope(float log2_theta, const double* __restrict__ turn, int q_len, int q_start,
-                                float2* __restrict__ cs) {
+// F: log2(theta), or (layers of starkv_load_plain) the frequencies in turns per position.
+template <typename F>
+__global__ void k_prefill_qrope(F freq, int q_len, int q_start, float2* __restrict__ cs) {
   const int idx = blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= q_len * 64) return;
   const int i = idx >> 6, p = idx & 63;
-  if (turn) {   // layers of starkv_load_plain: frequencies in turns per position
-    const double t = (double)(q_start + i) * turn[p];
-    float sn, c;
-    sincospif((float)(2.0 * (t - rint(t))), &sn, &c);
-    cs[idx] = make_float2(c, sn);
-    return;
-  }
-  const double ang = (double)(q_start + i) * exp2(-(2.0 * p / 128.0) * (double)log2_theta);
-  const double two_pi = 6.283185307179586476925286766559;
   float sn, c;
-  sincosf((float)(ang - two_pi * rint(ang / two_pi)), &sn, &c);
+  if constexpr (std::is_pointer_v<F>) {
+    const double t = (double)(q_start + i) * freq[p];
+    sincospif((float)(2.0 * (t - rint(t))), &sn, &c);
+  } else {
+    const double ang = (double)(q_start + i) * exp2(-(2.0 * p / 128.0) * (double)freq);
+    const double two_pi = 6.283185307179586476925286766559;
+    sincosf((float)(ang - two_pi * rint(ang / two_pi)), &sn, &c);
+  }
   cs[idx] = make_float2(c, sn);
 }
 
@@ -77,9 +78,12 @@ __global__ void k_prefill_qrope(float log2_theta, const double* __restrict__ tur
 // takes (row, 8-pair chunk) items of one head; the eight threads of a row are
 // neighbours in a warp, so a per-head norm of the query (layers of
 // starkv_load_plain that have one) is a sum over eight lanes.
-__global__ void __launch_bounds__(256) k_prefill_q(LayerView v, const __nv_bfloat16* __restrict__ q, int q_len,
+template <typename V>
+__global__ void __launch_bounds__(256) k_prefill_q(V v, const __nv_bfloat16* __restrict__ q, int q_len,
                                                   const float2* __restrict__ cs, int n_qt, uint8_t* __restrict__ Qt) {
   const int qt = blockIdx.x, h = blockIdx.y;
+  const float* w = nullptr;   // norm weights
+  if constexpr (std::is_same_v<V, ServeView>) w = v.q_norm;
   uint8_t* tile = Qt + ((size_t)h * n_qt + qt) * kTileB;
   for (int e = threadIdx.x; e < kT * 8; e += blockDim.x) {
     const int r = e >> 3, c8 = e & 7;   // row, pairs p = 8 c8 .. 8 c8 + 7 (and p + 64)
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(256) k_prefill_q(LayerView v, const __nv_bfloa
     const uint32_t aw[4] = {ra.x, ra.y, ra.z, ra.w}, bw[4] = {rb.x, rb.y, rb.z, rb.w};
     uint32_t lo[4], hi[4];
     float inv = 1.f;
-    if (v.q_norm) {
+    if (w) {
       float ss = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(256) k_prefill_q(LayerView v, const __nv_bfloa
       }
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      inv = 1.f / sqrtf(ss / 128.f + v.norm_eps);
+      if constexpr (std::is_same_v<V, ServeView>) inv = 1.f / sqrtf(ss / 128.f + v.norm_eps);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -109,9 +113,9 @@ __global__ void __launch_bounds__(256) k_prefill_q(LayerView v, const __nv_bfloa
       for (int x = 0; x < 2; ++x) {
         float a = __uint_as_float(x ? aw[k] & 0xFFFF0000u : aw[k] << 16);
         float b = __uint_as_float(x ? bw[k] & 0xFFFF0000u : bw[k] << 16);
-        if (v.q_norm) {
-          a *= inv * v.q_norm[c8 * 8 + 2 * k + x];
-          b *= inv * v.q_norm[64 + c8 * 8 + 2 * k + x];
+        if (w) {
+          a *= inv * w[c8 * 8 + 2 * k + x];
+          b *= inv * w[64 + c8 * 8 + 2 * k + x];
         }
         const float2 t = (v.rope && i < q_len) ? cs[(size_t)i * 64 + c8 * 8 + 2 * k + x] : make_float2(1.f, 0.f);
         re[x] = (a * t.x - b * t.y) * v.scale_log2;
@@ -214,8 +218,9 @@ __global__ void k_prefill_zv(LayerView v, const uint8_t* __restrict__ pool, long
 
 // ------------------------------------------------------------------ plain layers: stored K, V as tiles
 // K block of KV head g: [slot][128] bf16 (already rotated); V block:
-// [slot][H_kv 128] bf16; or both as 8 / 4-bit codes (kv_bits).  One CTA per (key tile, KV head); V is transposed
+// [slot][H_kv 128] bf16; or both as 8 / 4-bit codes (CODES).  One CTA per (key tile, KV head); V is transposed
 // through shared memory.
+template <bool CODES>
 __global__ void __launch_bounds__(256) k_prefill_plain_kv(LayerView v, const uint8_t* __restrict__ pool,
                                                          long long n_pages, const int32_t* __restrict__ pt_row,
                                                          int T, int n_kt, uint8_t* __restrict__ Kt,
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(256) k_prefill_plain_kv(LayerView v, const uin
         page = 0;
       }
       const uint8_t* base = pool + (size_t)page * v.page_bytes;
-      if (v.kv_bits) {
+      if constexpr (CODES) {
         // codes: the values they stand for, fp16 (code * scale stays below 32768 and is rounded once)
         uint32_t ko[4];
 #pragma unroll
@@ -301,9 +306,9 @@ struct GemmArgs {
   void* out;            // EPI_VT / EPI_KROPE: tiles [blockIdx.y][n_tiles]; EPI_OUT: row-major [rows][ld]
   int n_tiles;
   int rows, n_valid, ld;   // EPI_OUT
-  const int32_t* n_rows;   // EPI_OUT: rows in use (device; null: all)
   const uint8_t* E;        // EPI_KROPE: RoPE table (null: no rotation)
   uint32_t* status;
+  const int32_t* n_rows;   // EPI_OUT: rows in use (device; null: all)
 };
 
 template <int EPI>
@@ -330,10 +335,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_full(GemmArgs a) {
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_base;
-  tc::grid_launch_next();
+  if constexpr (EPI == EPI_OUT_BF16 || EPI == EPI_OUT_F32) tc::grid_launch_next();
   if (warp == 0) {
     if (lane == 0) {
-      tc::grid_wait_prev();
+      if constexpr (EPI == EPI_OUT_BF16 || EPI == EPI_OUT_F32) tc::grid_wait_prev();
       int k = 0;
       for (; k < a.KT; ++k) {
         const int s = k % a.stages;
@@ -882,13 +887,19 @@ cudaError_t launch_prefill_flash(const starkv_layer* L, const uint8_t* pool, lon
   PrefillWs w = prefill_ws_layout(L, ws, max_T, max_q);
   cudaError_t e;
   if (v.rope) {
-    k_prefill_qrope<<<(q_len * 64 + 255) / 256, 256, 0, s>>>(v.rope_log2_theta, v.turn, q_len, q_start, w.qcs);
+    const unsigned blocks = (q_len * 64 + 255) / 256;
+    if (L->view.turn) k_prefill_qrope<<<blocks, 256, 0, s>>>((const double*)L->view.turn, q_len, q_start, w.qcs);
+    else k_prefill_qrope<<<blocks, 256, 0, s>>>(v.rope_log2_theta, q_len, q_start, w.qcs);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  k_prefill_q<<<dim3(n_qt, v.H), 256, 0, s>>>(v, (const __nv_bfloat16*)q, q_len, w.qcs, n_qt_l, w.Qt);
+  if (L->view.opt)
+    k_prefill_q<<<dim3(n_qt, v.H), 256, 0, s>>>(L->view, (const __nv_bfloat16*)q, q_len, w.qcs, n_qt_l, w.Qt);
+  else
+    k_prefill_q<<<dim3(n_qt, v.H), 256, 0, s>>>(v, (const __nv_bfloat16*)q, q_len, w.qcs, n_qt_l, w.Qt);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (v.plain) {
-    k_prefill_plain_kv<<<dim3(n_kt, v.Hkv), 256, 0, s>>>(v, pool, n_pages, pt_row, T, n_kt_l, w.Kt, w.Vt);
+    (L->view.kv_bits ? k_prefill_plain_kv<true> : k_prefill_plain_kv<false>)<<<dim3(n_kt, v.Hkv), 256, 0, s>>>(
+        v, pool, n_pages, pt_row, T, n_kt_l, w.Kt, w.Vt);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   } else {
     // K = Zhat_k B'_k on the tensor cores, rotated in the epilogue

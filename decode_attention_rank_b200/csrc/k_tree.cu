@@ -74,7 +74,7 @@ struct TreeWs {
 };
 
 struct TreeMma {
-  LayerView v;
+  ServeView v;
   TreeArgs t;
   TreeWs w;
   int workers;           // warps (k_tree_mma) or CTAs (k_tree_tc) that share the units
@@ -130,7 +130,7 @@ __device__ __forceinline__ int warp_find(const T* off, int n, long long x, int l
 // them, with 1/16 for the odd ones (1: k_tree_mma, which meets 16 u there) or without (2: k_tree_tc).
 template <int BITS, int ORDER>
 __global__ void __launch_bounds__(128) k_tree_prep(TreeMma a) {
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const TreeArgs& t = a.t;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   tc::grid_wait_prev();
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
   using F = PageFmt<BITS>;
   constexpr int NS = MmaFmt<BITS, NT>::NS, RB = 8 * NT, QP = BITS == 0 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t ring_all[];
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const TreeArgs& t = a.t;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, j = lane & 3;
@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
   uint8_t* K_s = smem;
   uint8_t* V_s = smem + ST * kTcTile;
   uint8_t* R_s = smem + 2 * ST * kTcTile;   // codes
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const TreeArgs& t = a.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   tc::grid_wait_prev();
@@ -1389,7 +1389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
 // together.  Writes y as fp16 into the output product's B tiles; rows of no sequence and the tiles' padding rows are zero.
 template <int HPW>
 __global__ void __launch_bounds__(256, HPW == 1 ? 6 : 4) k_tree_combine(TreeMma a, int rows_pad, int NB, int KT) {
-  const LayerView& v = a.v;
+  const ServeView& v = a.v;
   const TreeArgs& t = a.t;
   const int lane = threadIdx.x & 31;
   const long long id = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
@@ -1480,7 +1480,7 @@ struct TreePlan {
 constexpr int kTcFrom = 25;
 
 TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
-  const LayerView& v = L->view;
+  const ServeView& v = L->view;
   TreePlan p;
   // Up to 256 rows the output product reads W_o once in an even split over the SMs; beyond, 128 x 128 tiles fill them (a whole call
   // over a short cache: 242 rows 41 us against 54, 400 rows 68 against 66, 820 rows 131 against 90).
@@ -1528,7 +1528,7 @@ cudaError_t launch_mma(const TreeMma& a, cudaStream_t s) {
 
 template <int BITS>
 cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cudaStream_t s) {
-  const LayerView& v = L->view;
+  const ServeView& v = L->view;
   cudaError_t e;
   const dim3 pgrid(a.t.n_nodes + 1, (v.H + kTreeWarps - 1) / kTreeWarps);
   if constexpr (BITS == 4) {
@@ -1555,7 +1555,7 @@ size_t tree_mma_ws_bytes(const starkv_layer* L, int batch, int n_nodes, int max_
 }
 
 cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, size_t ws_bytes, cudaStream_t s) {
-  const LayerView& v = L->view;
+  const ServeView& v = L->view;
   const TreePlan p = tree_plan(L, t.batch, t.n_nodes, t.max_nodes);
   if (ws_bytes < p.total) return cudaErrorInvalidValue;
   uint8_t* w = (uint8_t*)ws;

@@ -82,15 +82,20 @@ struct LayerView {
   float rope_log2_theta;      // log2(theta)
   float scale_log2;           // softmax scale * log2(e)
   long long page_bytes;
+  const LatentDesc* lat;      // device tables
+  const GroupDesc* grp;
+  uint32_t* status;
+};
+
+// And what starkv_load_plain adds.  Kernels that other layers run too take a LayerView, or both in two instances: with these
+// members in their parameters the compiler gave some of them more registers, and k_plain_decode took 6 % longer.
+struct ServeView : LayerView {
   int kv_bits;                // uncompressed layers: 0 = K and V stored in dtype, 8 or 4 = codes
   const float* q_norm;        // per-head norm weights [d] (null: none), see starkv_load_plain
   const float* k_norm;
   float norm_eps;
   const double* turn;         // RoPE frequencies in turns per position, theta^(-2p/d) / 2 pi (null without RoPE)
   int opt;                    // loaded by starkv_load_plain: queries are normed and rotated with `turn`
-  const LatentDesc* lat;      // device tables
-  const GroupDesc* grp;
-  uint32_t* status;
 };
 
 // Stored value of channel j of latent `ld` for token slot `slot` of a page block.
@@ -153,7 +158,7 @@ struct starkv_layer {
   std::vector<starkv::LatentDesc> lat;
   std::vector<starkv::GroupDesc> grp;
   std::vector<int> key_off;     // prefix sums of key widths, size Hkv + 1
-  starkv::LayerView view;
+  starkv::ServeView view;
   size_t page_bytes = 0;
   double bytes_per_token = 0;
   size_t factor_bytes = 0;
@@ -246,15 +251,18 @@ struct RowInfo {
   const int32_t* row_seq;   // [rows] sequence of each row, or null = identity
   const int32_t* row_len;   // [rows] visible tokens (decode: seq_lens)
   const int32_t* row_pos;   // [rows] RoPE position of the query, or null = len - 1
-  // rows that are nodes of drafted trees (null row_hist: none): slots below row_hist are visible, slot
-  // row_hist + j is where the row's mask has bit j (no mask: j <= row_node)
-  const int32_t* row_hist = nullptr;
-  const int32_t* row_node = nullptr;
-  const uint32_t* mask = nullptr;      // [rows][mask_words]
-  int mask_words = 0;
-  const int32_t* node_off = nullptr;   // first row of each sequence
-  const int32_t* node_pos = nullptr;   // [rows] RoPE positions of the nodes (their keys', too); null: queries are ready
-  const int32_t* n_rows = nullptr;     // rows in use: output rows from here on are not written
+};
+
+// Rows that are nodes of drafted trees: slots below row_hist are visible, slot row_hist + j is where the row's mask has
+// bit j (no mask: j <= row_node).
+struct TreeRows : RowInfo {
+  const int32_t* row_hist;
+  const int32_t* row_node;
+  const uint32_t* mask;      // [rows][mask_words]
+  int mask_words;
+  const int32_t* node_off;   // first row of each sequence
+  const int32_t* node_pos;   // [rows] RoPE positions of the nodes (their keys', too); null: queries are ready
+  const int32_t* n_rows;     // rows in use: output rows from here on are not written
 };
 
 // One sequence's drafted nodes, checked: rows off .. off + cnt - 1 of the call's node arrays, their K and V in slots
@@ -287,7 +295,7 @@ __device__ __forceinline__ bool tree_sees(const uint32_t* mask, int words, int r
 
 // K, V and queries of new tokens (k_kv.cu).
 struct KvArgs {
-  LayerView v;
+  ServeView v;
   uint8_t* pool;               // null: keys go to k_out
   long long n_pages;
   const int32_t* pt;
@@ -338,7 +346,7 @@ cudaError_t launch_tree_generic(const starkv_layer* L, const TreeArgs& t, void* 
 cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, long long n_pages,
                                   const int32_t* page_table, int max_pages, int rows, RowInfo ri, int max_len,
                                   const void* q, void* out, void* ws, size_t ws_bytes, bool prefill,
-                                  cudaStream_t s, bool tc_scores = false);
+                                  cudaStream_t s, bool tc_scores = false, const TreeRows* tree = nullptr);
 size_t decode_generic_ws_bytes(const starkv_layer* L, int rows, int max_len, bool prefill);
 
 // Uncompressed bf16 layers with head_dim 128: a streaming CUDA-core decode
