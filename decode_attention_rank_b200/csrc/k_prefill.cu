@@ -560,8 +560,8 @@ __device__ __forceinline__ void tmem_st_p(uint32_t taddr, const uint32_t* v) {
 
 __global__ void __launch_bounds__(kFlashThreads, 1) k_flash_prefill(FlashArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kKV], kv_empty[kKV], s_full[2], s_free[2], p_full, o_done,
-      o_free, fin;
+  __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kKV], kv_empty[kKV], s_full[2], s_free[2], p_full[2],
+      o_done[2], o_free, fin;
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
   __shared__ float xch[kSoftWarps][kT];   // per part and row: the part's row maximum, then its row sum
@@ -581,9 +581,11 @@ __global__ void __launch_bounds__(kFlashThreads, 1) k_flash_prefill(FlashArgs a)
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&s_full[s], 1);
       tc::mbar_init(&s_free[s], 4 * kSoftWarps);
+      // one per tile parity: a warp may be a tile ahead of another, so that on one barrier for both it would arrive twice in a
+      // phase, and take the phase before the last for the last (its parity is that of the one two before)
+      tc::mbar_init(&p_full[s], 4 * kSoftWarps);
+      tc::mbar_init(&o_done[s], 1);
     }
-    tc::mbar_init(&p_full, 4 * kSoftWarps);
-    tc::mbar_init(&o_done, 1);
     tc::mbar_init(&o_free, 4 * kSoftWarps);
     tc::mbar_init(&fin, 1);
     abort_flag = 0;
@@ -656,16 +658,16 @@ __global__ void __launch_bounds__(kFlashThreads, 1) k_flash_prefill(FlashArgs a)
           if (k + 1 == n_kt) tc::mma_commit(&q_empty);   // every S of this item issued: Q may be replaced
           // O += P(k) V(k); the first of an item overwrites O once the softmax has read the last item's
           if (k == 0 && !(ok = tc::mbar_wait_ab(&o_free, ((uint32_t)n & 1u) ^ 1u, a.status, &abort_flag))) break;
-          if (!(ok = tc::mbar_wait_ab(&p_full, (uint32_t)(jg + k) & 1u, a.status, &abort_flag))) break;
-          tc::tc_fence_after();
           const int pb = (jg + k) & 1;
+          if (!(ok = tc::mbar_wait_ab(&p_full[pb], ((uint32_t)(jg + k) >> 1) & 1u, a.status, &abort_flag))) break;
+          tc::tc_fence_after();
           const uint32_t vb = v_lo + (uint32_t)(((jg + k) % kKV) * kTileB >> 4);
           // A = P(j) from TMEM: K = 16 keys per MMA, 8 columns of fp16 pairs
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             tc::mma_f16_ts(tmem + o_col, tmem + (uint32_t)(pb * 128 + kk * 8),
                            vb + (uint32_t)(kk >> 2) * (kAtomB >> 4) + 2u * (kk & 3), hi, idesc, (k | kk) ? 1u : 0u);
-          tc::mma_commit(&o_done);
+          tc::mma_commit(&o_done[pb]);
           tc::mma_commit(&kv_empty[(jg + k) % kKV]);
         }
         jg += n_kt;
@@ -695,7 +697,8 @@ __global__ void __launch_bounds__(kFlashThreads, 1) k_flash_prefill(FlashArgs a)
       float m_used = -FLT_MAX, l = 0.f;
       for (int k = 0; k < n_kt; ++k) {
         const int j = jg + k, b = j & 1;
-        ok = ok && tc::mbar_wait_ab(&s_full[b], ((uint32_t)(j >> 1)) & 1u, a.status, &abort_flag);
+        // (by the whole warp: TMEM accesses are warp-wide)
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_ab(&s_full[b], ((uint32_t)(j >> 1)) & 1u, a.status, &abort_flag));
         tc::tc_fence_after();
         float s[kSoftCols];
         if (ok) {
@@ -747,10 +750,12 @@ __global__ void __launch_bounds__(kFlashThreads, 1) k_flash_prefill(FlashArgs a)
         const float ls = ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
         l = l * f + ls;
         // O is rescaled once the previous PV is done (rare: only when the
-        // maximum moved by more than the slack); o_done can then be at most
-        // one phase ahead of the one waited for, so skipping waits is safe
-        if (k > 0 && f != 1.f) {
-          ok = ok && tc::mbar_wait_ab(&o_done, ((uint32_t)(j - 1)) & 1u, a.status, &abort_flag);
+        // maximum moved by more than the slack).  Its barrier's phase before is
+        // PV(j - 3), complete since S(j) is, and PV(j + 1) needs this warp: the
+        // phase is the one meant, and skipping waits is safe.
+        if (k > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+          ok = __all_sync(0xffffffffu,
+                          ok && tc::mbar_wait_ab(&o_done[b ^ 1], ((uint32_t)(j - 1) >> 1) & 1u, a.status, &abort_flag));
           tc::tc_fence_after();
           if (ok) {
 #pragma unroll 1
@@ -771,10 +776,11 @@ __global__ void __launch_bounds__(kFlashThreads, 1) k_flash_prefill(FlashArgs a)
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&p_full);
+        if (lane == 0) tc::mbar_arrive(&p_full[b]);
       }
       jg += n_kt;
-      ok = ok && tc::mbar_wait_ab(&o_done, ((uint32_t)(jg - 1)) & 1u, a.status, &abort_flag);
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_ab(&o_done[(jg - 1) & 1], ((uint32_t)(jg - 1) >> 1) & 1u, a.status,
+                                                          &abort_flag));
       tc::tc_fence_after();
       // row sum over the parts
       xch[x][r] = l;

@@ -1,5 +1,6 @@
 """The serving operators over their whole range: values at both ends of what the codes hold, what a row sees of values
-that are not finite on every kernel, rows that see nothing, blocks of three row tiles.
+that are not finite on every kernel, rows that see nothing, blocks of three row tiles, prefills of many
+tiles.
 
 Tolerances of bf16 layers (check_tree): 3e-3 in relative L2, 1e-2 of the largest output.  The output's rounding is 1.6e-3;
 q, a weight, a dequantised value (|error| <= 2^-11 of itself, and none for scales below the smallest normal fp16, whose
@@ -281,4 +282,34 @@ def test_tree_of_17_to_24_rows(bits, H, hkv, counts):
     for masks in ([R.random_tree(rng, k)[0] for k in counts], None):
         got, want, _ = tree(p, c, hist, counts, masks, q)
         check_tree(got, want, "bf16")
+    assert p.L.sync_status() == 0
+
+
+# ------------------------------------------------------------------ prefill of many query tiles
+
+@pytest.mark.parametrize("bits,H,hkv,hist,n", [(8, 32, 8, 700, 1024), (0, 32, 8, 129, 700), (4, 40, 40, 1, 640)])
+def test_prefill_of_more_tiles_than_blocks(bits, H, hkv, hist, n):
+    """Several (query tile, head) items per block, so that a block's warps meet the next item's tiles while others still
+    write the last one's output: calls repeat to the bit, and rows at the tiles' edges and between are the definition's."""
+    p = Plain(H, hkv, 128, bits, norm=False)
+    c = p.cache([hist + n])
+    g = torch.Generator().manual_seed(n)
+    put(c, 0, *(torch.randn(hist + n, hkv, 128, generator=g, dtype=torch.float64) for _ in range(2)))
+    ws = torch.empty(p.L.workspace_bytes(1, c.pt.shape[1] * 16, n), dtype=torch.uint8, device="cuda").random_(0, 255)
+    out = torch.empty(n, p.hidden, dtype=p.dt, device="cuda")
+    c.upload()
+    for gain in (1.0, 6.0):                                      # 6: the running maximum moves by more than 8, O is rescaled
+        q = p.r(torch.randn(n, H, 128, generator=g) * gain)
+        qd = q.to(p.dt).cuda()
+        first = None
+        for _ in range(20):
+            out.fill_(7)
+            p.L.prefill(c.pool, c.n_pages, c.pt_d, [hist], [n], qd, out, ws)
+            first = out.clone() if first is None else first
+            assert torch.equal(out, first)
+        rows = sorted({0, 1, 127, 128, n // 2, n - 129, n - 2, n - 1} | set(range(5, n, 61)))
+        qx = p.norm_rope(q[rows], p.wq, torch.tensor(rows) + hist)
+        see = torch.arange(hist + n)[None] <= torch.tensor(rows)[:, None] + hist
+        want = R.attention(qx, c.K[0], c.V[0], see, 128 ** -0.5) @ p.W_o
+        check_tree(first[rows].to(torch.float64).cpu(), want, "bf16")
     assert p.L.sync_status() == 0
