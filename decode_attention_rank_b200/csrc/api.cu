@@ -612,7 +612,7 @@ starkv_status starkv_decode_attn(const starkv_layer* L, const void* pool, int64_
   size_t need = decode_generic_ws_bytes(L, batch, max_len, false) +
                 (L->tc_scores ? scores_tc_ws_bytes(L, batch, max_len) : 0);
   if (use_tc_all) need = decode_tc_ws_bytes(L, batch, max_len);
-  if (decode_by_tree(L)) need = tree_mma_ws_bytes(L, batch, batch, 1);
+  if (decode_by_tree(L)) need = tree_mma_need(L, batch, batch, 1);
   if (workspace == nullptr || ws_bytes < need) {
     set_error("decode workspace too small: need " + std::to_string(need) + " bytes");
     return STARKV_ERR_WORKSPACE;

@@ -202,7 +202,8 @@ starkv_status starkv_tree_attn(const starkv_layer* L, const void* pool, int64_t 
   CHECK_LAYER(L);
   const ServeView& v = L->view;
   CHECK_ARG(q_pos || v.plain || !v.rope, "a latent layer with RoPE needs q_pos");
-  const size_t need = starkv_tree_workspace_bytes(L, batch, max_pages * kPage, n_nodes, max_nodes);
+  const size_t need = tree_mma_supported(v) ? tree_mma_need(L, batch, n_nodes, max_nodes)
+                                            : tree_generic_need(L, max_pages * kPage, n_nodes);
   if (workspace == nullptr || ws_bytes < need) {
     set_error("tree workspace too small: need " + std::to_string(need) + " bytes");
     return STARKV_ERR_WORKSPACE;

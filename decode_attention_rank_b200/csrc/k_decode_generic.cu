@@ -540,8 +540,17 @@ size_t tree_tab_bytes(int n_nodes) {
 
 }  // namespace
 
+size_t tree_generic_need(const starkv_layer* L, int max_ctx, int n_nodes) {
+  size_t most = 0;   // of the full batches and the last one, whose fewer rows may take more splits
+  if (n_nodes >= kTreeRows) most = decode_generic_ws_bytes(L, kTreeRows, max_ctx, false);
+  if (n_nodes % kTreeRows) most = std::max(most, decode_generic_ws_bytes(L, n_nodes % kTreeRows, max_ctx, false));
+  return tree_tab_bytes(n_nodes) + most;
+}
+
 size_t tree_generic_ws_bytes(const starkv_layer* L, int max_ctx, int n_nodes) {
-  return tree_tab_bytes(n_nodes) + decode_generic_ws_bytes(L, std::min(n_nodes, kTreeRows), max_ctx, false);
+  size_t most = 0;
+  for (int r = 1; r <= std::min(n_nodes, kTreeRows); ++r) most = std::max(most, decode_generic_ws_bytes(L, r, max_ctx, false));
+  return tree_tab_bytes(n_nodes) + most;
 }
 
 // Every node as one row of the CUDA-core kernels, with its mask.
@@ -549,7 +558,7 @@ cudaError_t launch_tree_generic(const starkv_layer* L, const TreeArgs& t, void* 
   const int n = t.n_nodes, max_len = t.max_pages * kPage;
   int32_t* tab = (int32_t*)ws;
   const size_t tab_bytes = tree_tab_bytes(n);
-  if (ws_bytes < tree_generic_ws_bytes(L, max_len, n)) return cudaErrorInvalidValue;
+  if (ws_bytes < tree_generic_need(L, max_len, n)) return cudaErrorInvalidValue;
   k_tree_rows<<<(n + 127) / 128, 128, 0, s>>>(L->view, t.hist, t.node_off, t.batch, n, t.max_nodes, max_len, t.q_pos,
                                               tab, tab + n, tab + 2 * n, tab + 3 * n, tab + 4 * n, tab + 5 * n);
   cudaError_t e = cudaGetLastError();

@@ -1465,6 +1465,7 @@ template <int BITS, int NT>
 int mma_workers() { return MmaFmt<BITS, NT>::CTAS * kTreeWarps * num_sms(); }
 
 struct TreePlan {
+  size_t parts;          // partials
   size_t unit_off, item_off, q, row_b, pm, pl, pY, y, part, total;
   int NB, rows_pad;
   bool tc;               // k_tree_tc
@@ -1478,6 +1479,8 @@ struct TreePlan {
 // short sequences of 500 tokens 86 and 115 at 20 rows, 93 and 117 at 28, 137 and 132 at 64 (8 bits, 28 rows, by k_tree_tc: 104).
 // Lengths are known on the device only, so one number serves both.
 constexpr int kTcFrom = 25;
+
+size_t part_bytes(size_t parts, int rb) { return 2 * al256(parts * rb * 4) + al256(parts * rb * 512); }
 
 TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
   const ServeView& v = L->view;
@@ -1498,7 +1501,7 @@ TreePlan tree_plan(const starkv_layer* L, int batch, int n_nodes, int max_nodes)
   p.rb = p.tc ? kTcRows : 8 * p.nt;
   const size_t items = (size_t)v.Hkv * std::min((size_t)batch * ((max_nodes * v.group_q + p.rb - 1) / p.rb),
                                                 (size_t)batch + (size_t)n_nodes * v.group_q / p.rb);
-  const size_t parts = items + p.workers;
+  const size_t parts = p.parts = items + p.workers;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1550,8 +1553,26 @@ cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cu
 
 bool tree_mma_supported(const LayerView& v) { return v.plain && v.dtype == STARKV_BF16 && v.d == 128; }
 
-size_t tree_mma_ws_bytes(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
+size_t tree_mma_need(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
   return tree_plan(L, batch, n_nodes, max_nodes).total;
+}
+
+size_t tree_mma_ws_bytes(const starkv_layer* L, int batch, int n_nodes, int max_nodes) {
+  const ServeView& v = L->view;
+  const TreePlan p = tree_plan(L, batch, n_nodes, max_nodes);
+  const size_t own = part_bytes(p.parts, p.rb);
+  // Trees of fewer nodes may take blocks of other rows, with more partials in all; each kind of block needs the most with the
+  // most nodes that take it.  The other buffers grow with the batch and the nodes, but for the output product's partial
+  // sums, which only calls of up to 256 nodes have.
+  size_t most = own;
+  for (const int rows : {8, 16, kTcFrom - 1}) {
+    const int m = std::min(max_nodes, rows / v.group_q);
+    if (m < 1) continue;
+    const TreePlan q = tree_plan(L, batch, n_nodes, m);
+    most = std::max(most, part_bytes(q.parts, q.rb));
+  }
+  const size_t sums = p.full ? al256(outproj_part_bytes(L, 256)) : 0;
+  return p.total - own + most + sums;
 }
 
 cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, size_t ws_bytes, cudaStream_t s) {

@@ -339,8 +339,11 @@ struct TreeArgs {
   const int32_t* lens;         // decode: one query per sequence over lens[b] tokens (hist and node_off are null)
 };
 bool tree_mma_supported(const LayerView& v);
+// Workspace of a call, and the largest one of any call with no more sequences, nodes or nodes per sequence.
+size_t tree_mma_need(const starkv_layer* L, int batch, int n_nodes, int max_nodes);
 size_t tree_mma_ws_bytes(const starkv_layer* L, int batch, int n_nodes, int max_nodes);
 cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, size_t ws_bytes, cudaStream_t s);
+size_t tree_generic_need(const starkv_layer* L, int max_ctx, int n_nodes);
 size_t tree_generic_ws_bytes(const starkv_layer* L, int max_ctx, int n_nodes);
 cudaError_t launch_tree_generic(const starkv_layer* L, const TreeArgs& t, void* ws, size_t ws_bytes, cudaStream_t s);
 cudaError_t launch_decode_generic(const starkv_layer* L, const uint8_t* pool, long long n_pages,

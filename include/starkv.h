@@ -392,7 +392,10 @@ STARKV_API starkv_status starkv_tree_attn(const starkv_layer* layer, const void*
                                           int mask_words, const void* q, const int32_t* q_pos, void* out,
                                           void* workspace, size_t ws_bytes, starkv_stream_t stream);
 
-/* Workspace bytes of a starkv_tree_attn call; 0 for a NULL layer or sizes out of range. */
+/*
+ * Workspace bytes of a starkv_tree_attn call; 0 for a NULL layer or sizes out of range.  A buffer of this size serves every
+ * call with no more sequences, context, nodes or nodes per sequence, so one for the largest round serves all.
+ */
 STARKV_API size_t starkv_tree_workspace_bytes(const starkv_layer* layer, int batch, int max_ctx, int n_nodes,
                                               int max_nodes);
 

@@ -1,6 +1,6 @@
 """The serving operators over their whole range: values at both ends of what the codes hold, what a row sees of values
 that are not finite on every kernel, rows that see nothing, blocks of three row tiles, prefills of many
-tiles.
+tiles, and workspaces of the largest call.
 
 Tolerances of bf16 layers (check_tree): 3e-3 in relative L2, 1e-2 of the largest output.  The output's rounding is 1.6e-3;
 q, a weight, a dequantised value (|error| <= 2^-11 of itself, and none for scales below the smallest normal fp16, whose
@@ -313,3 +313,35 @@ def test_prefill_of_more_tiles_than_blocks(bits, H, hkv, hist, n):
         want = R.attention(qx, c.K[0], c.V[0], see, 128 ** -0.5) @ p.W_o
         check_tree(first[rows].to(torch.float64).cpu(), want, "bf16")
     assert p.L.sync_status() == 0
+
+
+# ------------------------------------------------------------------ workspaces
+
+@pytest.mark.parametrize("bits,dtype,H,hkv", [(8, "bf16", 32, 8), (0, "bf16", 32, 8), (4, "bf16", 8, 8), (0, "f32", 4, 1)])
+def test_workspace_of_the_largest_call_serves_smaller_ones(bits, dtype, H, hkv):
+    p = Plain(H, hkv, 128, bits, dtype, hidden=512)
+    L = p.L
+    sizes = dict(batch=[1, 3, 16], ctx=[16, 640, 4096], nodes=[1, 5, 16, 17, 63, 64, 65, 255, 256, 257, 512],
+                 most=[1, 2, 4, 5, 6, 7, 16, 32])
+    need = {(b, t, n, m): L.tree_workspace_bytes(b, t, n, m) for b in sizes["batch"] for t in sizes["ctx"]
+            for n in sizes["nodes"] for m in sizes["most"]}
+    for (b, t, n, m), x in need.items():
+        for (b2, t2, n2, m2), y in need.items():
+            if b2 <= b and t2 <= t and n2 <= n and m2 <= m:
+                assert y <= x, ((b, t, n, m), x, (b2, t2, n2, m2), y)
+    dec = [L.workspace_bytes(b, 640) for b in (1, 16, 64, 255, 256, 257, 300)]
+    assert dec == sorted(dec)
+    # the buffer of 512 nodes in trees of up to 32, for rounds of fewer
+    ws = torch.empty(L.tree_workspace_bytes(16, 48, 512, 32), dtype=torch.uint8, device="cuda")
+    g = torch.Generator().manual_seed(0)
+    for counts in ([16] * 16, [5] * 16, [1] * 16, [1, 0] * 8):
+        hist = [48 - 16] * 16
+        c = p.cache([48] * 16)
+        for b in range(16):
+            put(c, b, *(torch.randn(32 + counts[b], hkv, 128, generator=g, dtype=torch.float64) for _ in range(2)))
+        q = p.r(torch.randn(sum(counts), H, 128, generator=g))
+        _, want, args = tree(p, c, hist, counts, None, q)
+        args["out"].fill_(3)
+        L.tree_attn(**dict(args, workspace=ws))
+        check_tree(args["out"].to(torch.float64).cpu(), want, dtype)
+    assert L.sync_status() == 0
