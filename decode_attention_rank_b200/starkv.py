@@ -162,6 +162,18 @@ def _ints(t, n: int, name: str):
     return t.data_ptr()
 
 
+def _on_device(*tensors):
+    """Refuse tensors that are not on the current CUDA device: a kernel would follow their pointers all the same."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()                                 # -1: not on a CUDA device
+            if dev is None and d >= 0:
+                dev = _torch()._C._cuda_getDevice()
+            if d != dev:
+                raise ValueError(f"tensor {list(t.shape)} is on {t.device}, not on the current CUDA device")
+
+
 def _table(page_table, batch: int = 0):
     """Pointer, rows and columns of an int32 page table."""
     rows, cols = page_table.shape
@@ -305,6 +317,12 @@ class Layer:
                           c.n_kv_heads * c.head_dim)
         return self._dims
 
+    def _pool(self, pool, n_pages: int) -> int:
+        """Pointer of a pool of n_pages pages."""
+        if not pool.is_contiguous() or pool.nbytes < n_pages * self.page_bytes:
+            raise ValueError(f"pool must hold {n_pages} pages of {self.page_bytes} bytes, contiguous")
+        return pool.data_ptr()
+
     def qk_norm_rope(self, q, k, positions, q_out, k_out, stream=None) -> None:
         """Per-head norm and rotation of queries and keys (either pair may be None)."""
         dt, wq, wk = self._shape()
@@ -312,8 +330,10 @@ class Layer:
         n = int(some.shape[0]) if some is not None else 0
         (qp, ql), (kp, kl) = _rows(q, n, wq, "q", dt), _rows(k, n, wk, "k", dt)
         (qo, qol), (ko, kol) = _rows(q_out, n, wq, "q_out", dt), _rows(k_out, n, wk, "k_out", dt)
-        _check(_lib.starkv_qk_norm_rope(self._h, n, _ints(positions, n, "positions"), qp, ql, kp, kl, qo, qol, ko, kol,
-                                        _stream(stream)), "starkv_qk_norm_rope")
+        pos = _ints(positions, n, "positions")
+        _on_device(q, k, positions, q_out, k_out)
+        _check(_lib.starkv_qk_norm_rope(self._h, n, pos, qp, ql, kp, kl, qo, qol, ko, kol, _stream(stream)),
+               "starkv_qk_norm_rope")
 
     def append_qkv(self, pool, n_pages: int, page_table, seq_idx, slots, q, k, v, q_out=None, positions=None,
                    stream=None) -> None:
@@ -323,17 +343,20 @@ class Layer:
         (qp, ql), (kp, kl), (vp, vl) = _rows(q, n, wq, "q", dt), _rows(k, n, wk, "k", dt), _rows(v, n, wk, "v", dt)
         qo, qol = _rows(q_out, n, wq, "q_out", dt)
         pt, seqs, mp = _table(page_table)
-        _check(_lib.starkv_append_qkv(self._h, _ptr(pool), n_pages, pt, seqs, mp, n, _ints(seq_idx, n, "seq_idx"),
-                                      _ints(slots, n, "slots"), _ints(positions, n, "positions"), qp, ql, kp, kl, vp,
-                                      vl, qo, qol, _stream(stream)), "starkv_append_qkv")
+        si, sl, pos = _ints(seq_idx, n, "seq_idx"), _ints(slots, n, "slots"), _ints(positions, n, "positions")
+        _on_device(pool, page_table, seq_idx, slots, q, k, v, q_out, positions)
+        _check(_lib.starkv_append_qkv(self._h, self._pool(pool, n_pages), n_pages, pt, seqs, mp, n, si, sl, pos, qp, ql, kp,
+                                      kl, vp, vl, qo, qol, _stream(stream)), "starkv_append_qkv")
 
     def cache_read(self, pool, n_pages: int, page_table, seq_idx, slots, out, stream=None) -> None:
         """Cached tokens as dense rows [n, latent_total]."""
         dt, n = self._shape()[0], seq_idx.numel()
         op, _ = _rows(out, n, self.latent_total, "out", dt, dense=True)
         pt, seqs, mp = _table(page_table)
-        _check(_lib.starkv_cache_read(self._h, _ptr(pool), n_pages, pt, seqs, mp, n, _ints(seq_idx, n, "seq_idx"),
-                                      _ints(slots, n, "slots"), op, _stream(stream)), "starkv_cache_read")
+        si, sl = _ints(seq_idx, n, "seq_idx"), _ints(slots, n, "slots")
+        _on_device(pool, page_table, seq_idx, slots, out)
+        _check(_lib.starkv_cache_read(self._h, self._pool(pool, n_pages), n_pages, pt, seqs, mp, n, si, sl, op,
+                                      _stream(stream)), "starkv_cache_read")
 
     def tree_workspace_bytes(self, batch: int, max_ctx: int, n_nodes: int, max_nodes: int) -> int:
         return _lib.starkv_tree_workspace_bytes(self._h, batch, max_ctx, n_nodes, max_nodes)
@@ -351,10 +374,13 @@ class Layer:
         qp, _ = _rows(q, n, wq, "q", dt, dense=True)
         op, _ = _rows(out, n, self.cfg.hidden, "out", dt, dense=True)
         pt, _, mp = _table(page_table, batch)
-        _check(_lib.starkv_tree_attn(self._h, _ptr(pool), n_pages, pt, mp, batch, _ints(hist, batch, "hist"),
-                                     _ints(node_off, batch + 1, "node_off"), n, max_nodes,
-                                     _ints(mask, n * words, "mask"), words, qp, _ints(q_pos, n, "q_pos"), op,
-                                     _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+        hp, no = _ints(hist, batch, "hist"), _ints(node_off, batch + 1, "node_off")
+        mk, pos = _ints(mask, n * words, "mask"), _ints(q_pos, n, "q_pos")
+        _on_device(pool, page_table, hist, node_off, q, out, workspace, mask, q_pos)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        _check(_lib.starkv_tree_attn(self._h, self._pool(pool, n_pages), n_pages, pt, mp, batch, hp, no, n, max_nodes, mk,
+                                     words, qp, pos, op, workspace.data_ptr(), workspace.nbytes, _stream(stream)),
                "starkv_tree_attn")
 
     def tree_accept(self, pool, n_pages: int, page_table, hist, node_off, acc, n_acc, max_nodes: int,
@@ -363,9 +389,11 @@ class Layer:
         self._shape()
         batch, n = hist.numel(), acc.numel()
         pt, _, mp = _table(page_table, batch)
-        _check(_lib.starkv_tree_accept(self._h, _ptr(pool), n_pages, pt, mp, batch, _ints(hist, batch, "hist"),
-                                       _ints(node_off, batch + 1, "node_off"), n, max_nodes, _ints(acc, n, "acc"),
-                                       _ints(n_acc, batch, "n_acc"), _stream(stream)), "starkv_tree_accept")
+        hp, no = _ints(hist, batch, "hist"), _ints(node_off, batch + 1, "node_off")
+        ac, na = _ints(acc, n, "acc"), _ints(n_acc, batch, "n_acc")
+        _on_device(pool, page_table, hist, node_off, acc, n_acc)
+        _check(_lib.starkv_tree_accept(self._h, self._pool(pool, n_pages), n_pages, pt, mp, batch, hp, no, n, max_nodes, ac,
+                                       na, _stream(stream)), "starkv_tree_accept")
 
     def set_decode_path(self, path: int) -> None:
         """0 automatic, 1 CUDA-core kernels, 2 tensor-core scores + CUDA-core values (diagnostics)."""
@@ -413,9 +441,13 @@ def load_plain(cfg: LayerConfig, W_k, W_v, W_o, kv_bits: int = 0, q_norm=None, k
                stream=None) -> Layer:
     """Load an uncompressed layer with a quantised cache (kv_bits 8 or 4) and per-head query / key norms."""
     want = "torch.float32" if cfg.dtype == "f32" else "torch.bfloat16"
-    for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if t is not None and (str(t.dtype) != want or t.numel() != cfg.head_dim or not t.is_contiguous()):
-            raise ValueError(f"{name} must hold {cfg.head_dim} elements of the layer's dtype ({want})")
+    kv, qd = cfg.n_kv_heads * cfg.head_dim, cfg.n_heads * cfg.head_dim
+    given = (("W_k", W_k, cfg.hidden * kv), ("W_v", W_v, cfg.hidden * kv), ("W_o", W_o, qd * cfg.hidden),
+             ("q_norm", q_norm, cfg.head_dim), ("k_norm", k_norm, cfg.head_dim))
+    for name, t, n in given:
+        if t is not None and (str(t.dtype) != want or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{name} must hold {n} elements of the layer's dtype ({want}), contiguous")
+    _on_device(*(t for _, t, _ in given))
     c, keep = cfg._c()
     h = _vp()
     _check(_lib.starkv_load_plain(ctypes.byref(c), kv_bits, _ptr(q_norm), _ptr(k_norm), norm_eps, _ptr(W_k), _ptr(W_v),

@@ -163,3 +163,69 @@ def test_definition_of_attention_and_rotation():
     see = torch.tensor([[True, True], [False, True], [False, False]])
     out = R.attention(q.to(torch.float64), K, V, see, 1.0)
     assert out.tolist() == [[0.5, 0.5], [0.0, 1.0], [0.0, 0.0]]
+
+
+def fake_layer(sk, hkv=1, H=2, d=16):
+    """A layer without a handle: the library would answer that the layer is NULL."""
+    L = sk.Layer.__new__(sk.Layer)
+    L._h, L.page_bytes, L.latent_total = None, 64, 2 * hkv * d
+    L.cfg = sk.LayerConfig(hidden=64, n_heads=H, n_kv_heads=hkv, head_dim=d, plain=True)
+    return L
+
+
+def test_binding_refuses_host_tensors():
+    """Host memory of the right shapes and types is refused before any call of the library."""
+    from decode_attention_rank_b200 import starkv as sk
+    L = fake_layer(sk)
+    q, k = torch.zeros(3, 32, dtype=torch.bfloat16), torch.zeros(3, 16, dtype=torch.bfloat16)
+    i3, i2 = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    pt, pool = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(64, dtype=torch.uint8)
+    out = torch.zeros(3, 64, dtype=torch.bfloat16)
+    for call in (lambda: L.qk_norm_rope(q, k, i3, q, k, stream=0),
+                 lambda: L.append_qkv(pool, 1, pt, i3, i3, q, k, k, q_out=q, stream=0),
+                 lambda: L.cache_read(pool, 1, pt, i3, i3, torch.zeros(3, 32, dtype=torch.bfloat16), stream=0),
+                 lambda: L.tree_attn(pool, 1, pt, i2, i3, q, out, pool, max_nodes=2, stream=0),
+                 lambda: L.tree_accept(pool, 1, pt, i2, i3, i3, i2, max_nodes=2, stream=0)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    W = torch.zeros(64, 128, dtype=torch.bfloat16)
+    cfg = sk.LayerConfig(hidden=64, n_heads=1, n_kv_heads=1, head_dim=128, plain=True)
+    with pytest.raises(ValueError, match="CUDA device"):
+        sk.load_plain(cfg, W, W, W, stream=0)
+    for bad in (W[:63], W.float(), W.t()):
+        with pytest.raises(ValueError, match="W_v must hold"):
+            sk.load_plain(cfg, W, bad, W, stream=0)
+
+
+class OnDevice:
+    """A tensor that says that it is on a device."""
+
+    def __init__(self, t, dev):
+        self.t, self.dev = t, dev
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.dev
+
+
+def test_binding_refuses_another_device_and_a_short_pool(monkeypatch):
+    from decode_attention_rank_b200 import starkv as sk
+    L = fake_layer(sk)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    i3, i2 = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    pt, pool = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(64, dtype=torch.uint8)
+
+    def accept(dev, n_pages=1, pool_dev=1):
+        a = [OnDevice(x, 1) for x in (pt, i2, i3, i3, i2)]
+        a[3] = OnDevice(i3, dev)
+        L.tree_accept(OnDevice(pool, pool_dev), n_pages, *a, max_nodes=2, stream=0)
+
+    for dev, pool_dev in ((0, 1), (2, 1), (-1, 1), (1, 0), (0, 0)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            accept(dev, 1, pool_dev)
+    with pytest.raises(ValueError, match="pool must hold 2 pages"):
+        accept(1, 2)
+    with pytest.raises(sk.StarKVError, match="layer is NULL"):   # all as it should be: the library is asked
+        accept(1)
