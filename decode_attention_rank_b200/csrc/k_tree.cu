@@ -919,7 +919,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
   const TreeArgs& t = a.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   tc::grid_wait_prev();
-  tc::grid_launch_next();
   const long long U = a.w.unit_off[t.batch];
   const long long We = workers_used(a, U);
   const int w = blockIdx.x;
@@ -952,6 +951,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(TreeMma a) {
   tc::tc_fence_after();
   const uint32_t tmem = tmem_base;
   constexpr uint32_t o_col = 256, q_col = 384;
+  // Only now: a block of the output product that took TMEM of this SM first would keep it until the merge is done, and the
+  // merge waits for this kernel.
+  tc::grid_launch_next();
 
   if (warp == kTcMma) {
     // ------------------------------------------------ MMA issue
