@@ -618,6 +618,7 @@ starkv_status starkv_decode_attn(const starkv_layer* L, const void* pool, int64_
     return STARKV_ERR_WORKSPACE;
   }
   if (decode_by_tree(L)) {
+    CHECK_ARG(max_pages <= kTreeMaxPages, "max_pages * 16 + 128 overflows int");
     const TreeArgs t{(const uint8_t*)pool, n_pages, page_table, max_pages, batch, nullptr, nullptr, batch, 1, nullptr, 0,
                      q, q_pos, out, 1, seq_lens};
     CUDA_TRY(launch_tree_mma(L, t, workspace, ws_bytes, (cudaStream_t)stream));

@@ -191,7 +191,7 @@ starkv_status starkv_tree_attn(const starkv_layer* L, const void* pool, int64_t 
   if (batch == 0 || n_nodes == 0) return STARKV_OK;
   CHECK_ARG(pool && page_table && hist && node_off && q && out, "NULL buffer");
   CHECK_ARG(n_pages > 0 && max_pages > 0, "empty pool or page table");
-  CHECK_ARG(max_pages <= INT_MAX / kPage, "max_pages * 16 overflows int");
+  CHECK_ARG(max_pages <= kTreeMaxPages, "max_pages * 16 + 128 overflows int");
   CHECK_ARG(!mask || (mask_words >= 1 && mask_words <= kMaxNodes / 32 && mask_words * 32 >= max_nodes),
             "mask_words * 32 must cover max_nodes");
   CHECK_ARG(aligned_to(pool, 16) && aligned_to(q, 16) && aligned_to(out, 16) && aligned_to(workspace, 16),

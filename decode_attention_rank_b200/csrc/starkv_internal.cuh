@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -36,6 +37,8 @@ struct LatentDesc {
 };
 
 constexpr int kPage = 16;
+// Slots of a page table in the tree kernels: tile ends, up to 128 tokens further, must fit in an int.
+constexpr int kTreeMaxPages = (INT_MAX - 128) / kPage;
 
 // First bit of the code of (slot, channel i) inside a group's code block of n
 // channels at `bits` bits.  Key latents are slot-major: a token's codes of

@@ -378,6 +378,7 @@ STARKV_API starkv_status starkv_cache_read(const starkv_layer* layer, const void
  *     layers with RoPE need q_pos, and rotate the nodes' keys at q_pos too.
  *   out: [n_nodes][D] in dtype.  Rows from node_off[batch] on are left as they are.
  *   workspace: starkv_tree_workspace_bytes(layer, batch, max_pages * 16, n_nodes, max_nodes) bytes.
+ *   max_pages * 16 + 128 must fit in an int (starkv_decode_attn over codes: too).
  * A sequence with more than max_nodes nodes, or whose rows or slots leave
  * [0, n_nodes) or the page table, sets STARKV_DEV_BAD_POSITION and its rows are
  * zero; a node_off that decreases does so for every row.

@@ -229,3 +229,13 @@ def test_binding_refuses_another_device_and_a_short_pool(monkeypatch):
         accept(1, 2)
     with pytest.raises(sk.StarKVError, match="layer is NULL"):   # all as it should be: the library is asked
         accept(1)
+
+
+def test_tree_page_tables_whose_tiles_would_pass_the_largest_int():
+    """A length is rounded up to a tile of 128 tokens: tables within 128 of 2^31 slots are refused, below they are not."""
+    r, (b, p) = raw(), buf()
+    most = (2 ** 31 - 1 - 128) // 16
+    for pages in (most + 1, (2 ** 31 - 1) // 16):
+        assert r.starkv_tree_attn(p, p, 1, p, pages, 1, p, p, 1, 1, None, 0, p, None, p, p, 1, None) == 1 and "overflows" in err()
+    # (the next check of the call is the alignment of q)
+    assert r.starkv_tree_attn(p, p, 1, p, most, 1, p, p, 1, 1, None, 0, p + 8, None, p, p, 1, None) == 1 and "aligned" in err()
