@@ -467,8 +467,10 @@ cudaError_t launch_qkv_d(const KvArgs& a, cudaStream_t s) {
   const int gq = (a.v.H + RPW - 1) / RPW, gk = (a.v.Hkv + RPW - 1) / RPW;
   const int groups = (a.q ? gq : 0) + (a.k ? gk : 0) + (a.vv ? gk : 0);
   // Many tokens: one CTA for a whole token, four warps (they share the angles and keep their factors over several groups).
-  // Few: a row group per warp, the token over several CTAs, for latency.
-  const bool many = (long long)a.n * groups > 64LL * num_sms();
+  // Few: a row group per warp, the token over several CTAs, for latency.  Few / many, us: norm and rotation of 32 + 8 heads, bf16,
+  // 192 tokens 3.0 / 3.5, 256 3.9 / 3.5, 384 4.5 / 3.7, 768 7.6 / 4.8; 16 + 16 heads 256 2.9 / 3.3, 512 4.8 / 3.9; fp32 192 4.0 / 3.9, 384
+  // 5.6 / 4.3; append of 32 heads over 8 bits 256 9.6 / 10.6, 384 12.6 / 12.1.  The sides meet at 190 to 410 tokens.
+  const bool many = a.n > 2 * num_sms();
   const int nw = std::min(many ? 4 : NW, groups), per = many ? (groups + nw - 1) / nw : 1;
   return launch_k(k_qkv<T, D, BITS>, dim3((unsigned)a.n, (unsigned)((groups + nw * per - 1) / (nw * per))), 32 * nw, 0, s, true,
                   a, groups, per);

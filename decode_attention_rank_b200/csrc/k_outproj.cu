@@ -196,8 +196,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) k_outproj_tc(OutArgs a) {
   if (warp == 1) tc::tmem_dealloc(tmem, a.tmem_cols);
 }
 
-// out[row][n] = sum over the CTAs whose k-range touched output tile n / 128.  A block takes PER rows: one for
-// few rows (as many blocks as there are), four for many.
+// out[row][n] = sum over the CTAs whose k-range touched output tile n / 128.  A block takes PER rows: one up to 48 rows (as
+// many blocks as there are), four beyond.  A whole tree call over 31 tokens, one / four rows, us: 17 rows 21.3 / 22.2, 33 22.6 / 23.0,
+// 48 23.2 / 23.3, 64 24.8 / 23.8, 128 33.2 / 30.6, 256 47.0 / 41.0.
 template <typename TO, int PER>
 __global__ void k_outproj_reduce(const float* __restrict__ part, int G, int KT, int DT, int slots, int NB, int rows,
                                  int D, const int32_t* __restrict__ n_rows, TO* __restrict__ out) {
@@ -326,8 +327,8 @@ cudaError_t launch_gemm_tc(const uint8_t* Mt, int n_out, int K, int n_valid, con
   };
   using One = std::integral_constant<int, 1>;
   using Four = std::integral_constant<int, 4>;
-  if (out_f32) return rows > 32 ? reduce((float*)out, Four{}) : reduce((float*)out, One{});
-  return rows > 32 ? reduce((__nv_bfloat16*)out, Four{}) : reduce((__nv_bfloat16*)out, One{});
+  if (out_f32) return rows > 48 ? reduce((float*)out, Four{}) : reduce((float*)out, One{});
+  return rows > 48 ? reduce((__nv_bfloat16*)out, Four{}) : reduce((__nv_bfloat16*)out, One{});
 }
 
 cudaError_t launch_outproj_tc(const starkv_layer* L, const void* y_tiles, int rows, void* out, float* part,

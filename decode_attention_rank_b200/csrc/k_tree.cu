@@ -41,7 +41,10 @@ namespace starkv {
 namespace {
 
 constexpr int kTreeWarps = 4;          // warps per CTA
-constexpr int kMinUnits = 2;           // pages of a warp's run, at least (short calls use fewer warps)
+// Pages of a warp's run, at least (short calls use fewer warps).  Runs of 1 / 2 / 4, a whole call over 8 bits, us: one token over 100 15.3 /
+// 16.6 / 17.9 (8 KV heads), 7 nodes over 333 18.3 / 18.3 / 19.7 (32), 4 x 7 over 200 25.7 / 25.2 / 25.0 (32), 4 over 1000 22.2 / 22.2 /
+// 24.3 (8), 16 x 1 over 500 24.5 / 24.5 / 22.6 (8).
+constexpr int kMinUnits = 2;
 constexpr int kTcRows = 128;           // rows of a row block of k_tree_tc
 constexpr int kTcTok = 128;            // tokens of its tiles
 
@@ -1602,7 +1605,9 @@ cudaError_t launch_tree_mma(const starkv_layer* L, const TreeArgs& t, void* ws, 
   cudaError_t e = v.kv_bits == 8 ? launch_bits<8>(L, a, p, s) : v.kv_bits == 4 ? launch_bits<4>(L, a, p, s)
                                                                                : launch_bits<0>(L, a, p, s);
   if (e != cudaSuccess) return e;
-  // a warp per head while that fills the SMs at most twice; else a row's heads share their row's lookups
+  // A warp per head while that fills the SMs at most twice; else a row's heads share their row's lookups.  A warp per head / per four, a
+  // whole call with 32 heads over 31 tokens, us: 16 rows 16.4 / 17.1, 128 30.5 / 33.0, 512 74.6 / 76.5, 592 79.7 / 77.6, 1024 116 / 113; over
+  // 500 tokens 16 rows 24.7 / 37.6, 512 146 / 144.
   const bool few = (long long)p.rows_pad * v.H <= 128LL * num_sms();
   const long long warps = (long long)p.rows_pad * (few ? v.H : (v.H + 3) / 4);
   e = launch_k(few ? k_tree_combine<1> : k_tree_combine<4>, (unsigned)((warps * 32 + 255) / 256), 256, 0, s, true, a, p.rows_pad,
