@@ -262,7 +262,8 @@ __device__ __forceinline__ void load_w(const float* w, int half, int c, float* w
 // queries' groups, then the keys', then the values'); its warps take them in turn, the next group's rows loaded before this
 // one's are worked on.  The token's cos / sin are made once per CTA; a lane's channels are the same in every head, so it
 // keeps its factors in registers.  Angles: the fraction of the turn in 64 bits, then an fp32 sincos; in 64 bits
-// throughout for keys that are quantised next.  Measured: 4096 tokens of 32 + 32 heads in 28.6 us (4.7 TB/s; bytes, then issue);
+// throughout for keys that are quantised next.  Measured: 4096 tokens of 32 + 32 heads in 28.6 us (4.7 TB/s; waits for loads, with
+// 21 warps an SM, by registers; issue in 43 % of the cycles);
 // 8193 tokens of 32 + 8 heads into 4 bits in 56 us (issue: 4,170 instructions a token).
 template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(kKvThreads, 3) k_qkv(KvArgs a, int groups, int per) {

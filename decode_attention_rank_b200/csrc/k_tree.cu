@@ -10,10 +10,13 @@
 //   scores   S^T = K Q^T.  A code byte u under the fp16 exponent of 1024 is the number 1024 + u (one PRMT per two codes;
 //            4-bit codes in a word's high nibbles come out as 1024 + 16 u, their q is 1/16).  A group's accumulator starts
 //            at -sum_c q_c (1024 + 2^(b-1)), so it ends at sum_c q_c (u - 2^(b-1)); then S += scale[token][group] * it.
-//            |offset| is below 40 times the sum, whose fp32 rounding stays below 2^-17 of q's length times a code.
+//            What cancels is far larger than what is left, so its rounding counts: the sums on the way are at most 1279 sum|q_c|
+//            over a group of 8 bits (1039 over 4), and each fp32 rounding of one is off by 2^-24 of that, 7.6e-5 (6.2e-5)
+//            sum|q_c| <= 4.3e-4 (3.5e-4) |q| codes.  A group's key is at least 126 (7) codes long, which makes it 3.4e-6 (5e-5)
+//            of |q||k| at most; with codes spread evenly 1.0e-6 (1.5e-5).  (q's own rounding to fp16 is 2.8e-4 a channel.)
 //   values   Y^T = V^T P^T.  P is transposed by one movmatrix per 8 tokens.  The codes become exact integers (the offset taken
 //            off by one packed subtraction; it cannot be folded into the accumulator here, whose sum over thousands of tokens
-//            would cancel) and are multiplied by their token's scale in fp16.  |code * scale| <= 32768 fits, and as every scale
+//            would cancel) and are multiplied by their token's scale in fp16.  |code * scale| stays below 32800, and as every scale
 //            is a multiple of 2^-24 so is every product: the rounding is 2^-11 of it at most, however small the scale.  (P * scale
 //            instead, with 2 NT products a group for 8, leaves fp16 at both ends: 2^7 * 4681, the largest scale of 4 bits, is
 //            infinite, and a weight 2^-12 of the largest is lost beside values of 1e-3.  It took 97.4 us for one token each of 16
@@ -741,8 +744,9 @@ __global__ void __launch_bounds__(32 * kTreeWarps, MmaFmt<BITS, NT>::CTAS) k_tre
 //                 exponentials run beside the other's loads and maxima.  The row's running maximum is handed from tile to
 //                 tile through shared memory as soon as it is known; rows past the block's are skipped by the warp.  P
 //                 overwrites S in TMEM; O is rescaled when the maximum grew by more than 2^8.
-// Measured: 64 trees of 24 over 8K, 4 bits, 32 heads on 8 KV heads in 354 us (blocks of 16 rows in k_tree_mma's way: 1,213 us). Bound
-// by issue slots, about 1,800 a scheduler and tile; the products alone would take 1,300 cycles a tile.
+// Measured: 64 trees of 24 over 8K, 4 bits, 32 heads on 8 KV heads in 354 us (blocks of 16 rows in k_tree_mma's way: 1,213 us).  About
+// 1,800 issue slots a scheduler and tile, 55 % of the cycles; the products alone would take 1,300 cycles a tile.  The softmax warps read S
+// twice, since 20 warps leave a thread 96 registers (over codes 124 bytes of spills as it is).
 // TMEM: S in two 128-column buffers, O in 256 .. 383, Q in 384 .. 447.  Units of work: tiles, dealt to the CTAs as above.
 // bf16 caches: K and V are operands as they lie, so warps 0 - 7 copy them straight into three stages of tiles.  Q and P enter as
 // a high and a low bf16 part (one rounding of P to bf16 would show in the output), in TMEM columns 384 .. 511 and in place, 16
@@ -1550,8 +1554,9 @@ cudaError_t launch_bits(const starkv_layer* L, TreeMma& a, const TreePlan& p, cu
     return launch_k(k_tree_tc<BITS>, a.workers, kTcThreads, TcFmt<BITS>::SMEM, s, true, a);
   }
   if (p.nt == 1) return launch_mma<BITS, 1>(a, s);
-  if (p.nt == 2 || BITS == 0) return launch_mma<BITS, 2>(a, s);
-  return launch_mma<BITS == 0 ? 8 : BITS, 3>(a, s);
+  if constexpr (BITS != 0)
+    if (p.nt == 3) return launch_mma<BITS, 3>(a, s);
+  return launch_mma<BITS, 2>(a, s);
 }
 
 }  // namespace

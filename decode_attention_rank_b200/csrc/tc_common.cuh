@@ -39,8 +39,10 @@ __device__ __host__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk)
 }
 
 // ---- programmatic dependent launch ------------------------------------------
-// (Both do nothing in a launch without the attribute.)  grid_launch_next lets the next kernel's blocks start as
-// resources come free; grid_wait_prev returns when the kernels before have completed and their writes are visible.
+// grid_launch_next lets the next kernel's blocks start as resources come free, if that launch has the attribute (whether this
+// one has it does not matter); grid_wait_prev returns when the kernels before have completed and their writes are visible, at
+// once in a launch without the attribute.  So a kernel that is launched early waits before it touches anything that an earlier
+// kernel reads or writes, whatever way those were launched.
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait_prev() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
