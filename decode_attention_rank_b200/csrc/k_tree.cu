@@ -13,7 +13,7 @@
 //            What cancels is far larger than what is left, so its rounding counts: the sums on the way are at most 1279 sum|q_c|
 //            over a group of 8 bits (1039 over 4), and each fp32 rounding of one is off by 2^-24 of that, 7.6e-5 (6.2e-5)
 //            sum|q_c| <= 4.3e-4 (3.5e-4) |q| codes.  A group's key is at least 126 (7) codes long, which makes it 3.4e-6 (5e-5)
-//            of |q||k| at most; with codes spread evenly 1.0e-6 (1.5e-5).  (q's own rounding to fp16 is 2.8e-4 a channel.)
+//            of |q||k| at most; with codes spread evenly 1.0e-6 (1.5e-5).  (q's own rounding to fp16: 2^-11 of a channel.)
 //   values   Y^T = V^T P^T.  P is transposed by one movmatrix per 8 tokens.  The codes become exact integers (the offset taken
 //            off by one packed subtraction; it cannot be folded into the accumulator here, whose sum over thousands of tokens
 //            would cancel) and are multiplied by their token's scale in fp16.  |code * scale| stays below 32800, and as every scale
