@@ -580,10 +580,10 @@ size_t starkv_workspace_bytes(const starkv_layer* L, int batch, int max_ctx, int
   if (decode_by_tree(L)) need = std::max(need, tree_mma_ws_bytes(L, batch, batch, 1));
   if (L->tc_scores) need += scores_tc_ws_bytes(L, batch, max_ctx);
   if (L->tc_values) need = std::max(need, decode_tc_ws_bytes(L, batch, max_ctx));
+  const long long rows = std::min<long long>((long long)batch * max_q, 1 << 30);
+  // (one query each, too: the row kernels' table comes on top of a decode's buffers)
+  need = std::max(need, ru(sizeof(int32_t) * 3 * (size_t)rows, 256) + decode_generic_ws_bytes(L, (int)rows, max_ctx, true));
   if (max_q > 1) {
-    const long long rows = std::min<long long>((long long)batch * max_q, 1 << 30);
-    need = std::max(need, ru(sizeof(int32_t) * 3 * (size_t)rows, 256) +
-                              decode_generic_ws_bytes(L, (int)rows, max_ctx, true));
     if (L->tc_scores && L->tc_values)
       need = std::max(need, prefill_tc_ws_bytes(L, rows, (max_ctx + kPage - 1) / kPage));
     if (prefill_flash_supported(L)) need = std::max(need, prefill_flash_ws_bytes(L, max_ctx, max_q));

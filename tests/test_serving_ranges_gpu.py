@@ -345,3 +345,24 @@ def test_workspace_of_the_largest_call_serves_smaller_ones(bits, dtype, H, hkv):
         L.tree_attn(**dict(args, workspace=ws))
         check_tree(args["out"].to(torch.float64).cpu(), want, dtype)
     assert L.sync_status() == 0
+
+
+@pytest.mark.parametrize("bits,dtype,d", [(8, "bf16", 128), (4, "bf16", 64), (0, "bf16", 128), (0, "f32", 128)])
+def test_prefill_of_one_query_each_in_its_workspace(bits, dtype, d):
+    """Workspace sizes of max_q = 1 serve a prefill of one query per sequence, over short tables too."""
+    p = Plain(4, 2, d, bits, dtype, norm=False)
+    for lens in ([1], [9, 30, 16], [40]):
+        B = len(lens)
+        c = p.cache(lens)
+        g = torch.Generator().manual_seed(B)
+        for b, T in enumerate(lens):
+            put(c, b, *(torch.randn(T, 2, d, generator=g, dtype=torch.float64) for _ in range(2)))
+        q = p.r(torch.randn(B, 4, d, generator=g))
+        out = torch.empty(B, p.hidden, dtype=p.dt, device="cuda")
+        ws = torch.empty(p.L.workspace_bytes(B, c.pt.shape[1] * 16, 1), dtype=torch.uint8, device="cuda")
+        p.L.prefill(c.upload(), c.n_pages, c.pt_d, [T - 1 for T in lens], [1] * B, q.to(p.dt).cuda(), out, ws)
+        qx = p.norm_rope(q, None, torch.tensor(lens) - 1)
+        want = torch.cat([R.attention(qx[b:b + 1], c.K[b], c.V[b], torch.ones(1, T, dtype=torch.bool), d ** -0.5) @ p.W_o
+                          for b, T in enumerate(lens)])
+        check_tree(out.to(torch.float64).cpu(), want, dtype)
+    assert p.L.sync_status() == 0
